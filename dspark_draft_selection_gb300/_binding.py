@@ -18,7 +18,8 @@ c_i32, c_i64, c_f32, c_vp, c_sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 DSPARK_BF16, DSPARK_F32 = 0, 1
 DSPARK_MAXSUM, DSPARK_WALK, DSPARK_SAMPLE = 0, 1, 2
-OP_TOPK, OP_LATTICE, OP_CHAIN, OP_SAMPLE, OP_DENSE_WALK, OP_VERIFY, OP_D2T_CHECK, OP_LATTICE_ROW = range(8)
+OP_TOPK, OP_LATTICE, OP_CHAIN, OP_SAMPLE, OP_DENSE_WALK, OP_VERIFY, OP_D2T_CHECK, OP_LATTICE_ROW, \
+    OP_TREE_ATTENTION = range(9)
 STATUS = {0: "DSPARK_OK", 1: "DSPARK_EINVAL", 2: "DSPARK_ERANGE", 3: "DSPARK_EDUP", 4: "DSPARK_EPROPOSAL",
           5: "DSPARK_ENONFINITE", 6: "DSPARK_ETIMEOUT", 7: "DSPARK_ECUDA", 8: "DSPARK_EWORKSPACE"}
 MODES = {"maxsum": DSPARK_MAXSUM, "walk": DSPARK_WALK, "sample": DSPARK_SAMPLE}
@@ -49,6 +50,13 @@ SIGNATURES = [
                                   c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
     ("dspark_verify", c_i32, [c_vp, c_i32, c_i64, c_i32, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_f32,
                               c_f32, c_f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    ("dspark_tree_mask", c_i32, [c_vp, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp]),
+    ("dspark_rope_append", c_i32, [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_i32, c_i32, c_vp, c_i32, c_vp, c_i64,
+                                   c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp]),
+    ("dspark_tree_attention", c_i32, [c_vp, c_i64, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_f32, c_f32, c_vp,
+                                      c_i64, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    ("dspark_tree_accept", c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    ("dspark_cache_commit", c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp]),
 ]
 
 
@@ -61,6 +69,13 @@ class QRecord(ctypes.Structure):
 class Penalties(ctypes.Structure):
     """dspark_penalties: the history and the repetition / presence penalties of a walk."""
     _fields_ = [("ids", c_vp), ("n", c_vp), ("cap", c_i32), ("repetition", c_f32), ("presence", c_f32)]
+
+
+class KVCache(ctypes.Structure):
+    """dspark_kvcache: a paged key/value cache (two buffers of one layout) and its page table."""
+    _fields_ = [("k", c_vp), ("v", c_vp), ("dtype", c_i32), ("n_layers", c_i32), ("layer_stride", c_i64),
+                ("page_stride", c_i64), ("token_stride", c_i64), ("head_stride", c_i64), ("num_pages", c_i64),
+                ("page_size", c_i32), ("heads", c_i32), ("head_dim", c_i32), ("page_table", c_vp), ("ld_table", c_i32), ("table_pages", c_i32)]
 
 
 class DsparkError(RuntimeError):
@@ -404,3 +419,140 @@ def dspark_verify(tgt_logits, B, draft_tgt, n_draft, q, *, V_q=None, q_d2t=None,
                                _p(vseed), _p(step), _p(out[0]), _p(out[1]), _p(out[2]), wp, wn, _p(status),
                                _stream(stream)), "dspark_verify")
     return out + (status,)
+
+
+def _kvcache(k, v, page_table):
+    """KVCache of k, v [(layers,) pages, page, heads, head_dim] (any strides, the last 1) and page_table [R, n]."""
+    shape, st = k.shape, k.stride()
+    if v.shape != shape or v.stride() != st or v.dtype != k.dtype:
+        raise ValueError("keys and values are of one shape, layout and type")
+    if len(shape) not in (4, 5) or st[-1] != 1:
+        raise ValueError("expected [(layers,) pages, page, heads, head_dim] with unit column stride")
+    if page_table.dim() != 2 or page_table.stride(1) != 1 or page_table.dtype != torch.int32:
+        raise ValueError("expected an int32 page table [R, pages] with unit column stride")
+    layers, lst = (shape[0], st[0]) if len(shape) == 5 else (1, 0)
+    return KVCache(_p(k), _p(v), _dt(k), layers, lst, st[-4], st[-3], st[-2], shape[-4], shape[-3], shape[-2], shape[-1],
+                   _p(page_table), max(page_table.stride(0), page_table.shape[1]), page_table.shape[1])
+
+
+def _node_rows(t, dtype=None):
+    """Row stride of [R, T, heads, head_dim] whose heads lie side by side, the rows of all requests at one stride."""
+    R, T, H, D = t.shape
+    st = t.stride()
+    if (D > 1 and st[3] != 1) or (H > 1 and st[2] != D) or (R > 1 and T > 1 and st[0] != T * st[1]):
+        raise ValueError("expected [R, T, heads, head_dim] with heads side by side and one row stride")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"expected {dtype}, got {t.dtype}")
+    return st[1] if T > 1 else st[0] if R > 1 else H * D
+
+
+def _i32(t, *shape):
+    """Pointer of a contiguous int32 device tensor of this shape (None: no tensor)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"expected a contiguous int32 tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    return _p(t)
+
+
+def dspark_tree_mask(parent, *, R=None, T=None, n_nodes=None, base=None, out=None, status=None, stream=None, device="cuda"):
+    """Ancestor mask and positions of drafted trees: parent [R, T] int32 (None: chains of R x T) ->
+    (mask [R, T, W] int32 words, pos [R, T] int32, status)."""
+    if parent is not None:
+        R, T = parent.shape
+        device = parent.device
+    if out is None:
+        out = (torch.empty((R, T, (T + 31) // 32), dtype=torch.int32, device=device),
+               torch.empty((R, T), dtype=torch.int32, device=device))
+    status = new_status(device) if status is None else status
+    _check(lib().dspark_tree_mask(_i32(parent, R, T), _i32(n_nodes, R), _i32(base, R), R, T,
+                                  _i32(out[0], R, T, (T + 31) // 32), _i32(out[1], R, T), _p(status), _stream(stream)),
+           "dspark_tree_mask")
+    return out[0], out[1], status
+
+
+def dspark_rope_append(q, k, v, pos, cos_sin, k_cache, v_cache, page_table, ctx_len, *, axis=None, n_nodes=None,
+                       interleaved=False, out=None, status=None, stream=None):
+    """Turns q [R, T, Hq, D] and k [R, T, H, D] by their positions pos [R, T] or [R, T, axes] (table cos_sin
+    [P, rot] float32, axis [rot / 2] int32) and writes k and v to the nodes' slots of the paged cache.
+    Returns (q_out, status); out may be q itself."""
+    R, T, Hq, D = q.shape
+    c = _kvcache(k_cache, v_cache, page_table)
+    H = c.heads
+    if k.shape != (R, T, H, D) or v.shape != k.shape or D != c.head_dim or page_table.shape[0] != R:
+        raise ValueError("q, k, v, the cache and its page table do not fit together")
+    out = torch.empty((R, T, Hq, D), dtype=q.dtype, device=q.device) if out is None else out
+    if out.shape != q.shape:
+        raise ValueError("out has another shape than q")
+    status = new_status(q.device) if status is None else status
+    A = 1 if pos.dim() == 2 else pos.shape[2]
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("expected a contiguous float32 table cos_sin [P, rot]")
+    P, rot = cos_sin.shape
+    _check(lib().dspark_rope_append(_p(q), _node_rows(q, k_cache.dtype), _p(k), _node_rows(k, k_cache.dtype), _p(v),
+                                    _node_rows(v, k_cache.dtype), R, T, Hq,
+                                    _i32(pos, R, T) if pos.dim() == 2 else _i32(pos, R, T, A), A, _p(cos_sin), P, rot,
+                                    _i32(axis, rot // 2), int(interleaved), ctypes.byref(c), _i32(ctx_len, R),
+                                    _i32(n_nodes, R), _p(out), _node_rows(out, k_cache.dtype), _p(status),
+                                    _stream(stream)), "dspark_rope_append")
+    return out, status
+
+
+def dspark_tree_attention(q, k_cache, v_cache, page_table, ctx_len, *, mask=None, n_nodes=None, scale=None, softcap=0.0,
+                          out=None, lse=None, ws=None, status=None, stream=None):
+    """Attention of the nodes' queries q [R, T, Hq, D] over the committed slots and the nodes that mask
+    [R, T, W] shows (None: chains). lse: None (allocated), a float32 [R, T, Hq] tensor, or False (not
+    written). Returns (out, lse, status)."""
+    R, T, Hq, D = q.shape
+    c = _kvcache(k_cache, v_cache, page_table)
+    if D != c.head_dim or page_table.shape[0] != R:
+        raise ValueError("q, the cache and its page table do not fit together")
+    dev = q.device
+    out = torch.empty((R, T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+    if out.shape != q.shape:
+        raise ValueError("out has another shape than q")
+    if lse is None:
+        lse = torch.empty((R, T, Hq), dtype=torch.float32, device=dev)
+    elif lse is False:
+        lse = None
+    elif lse.shape != (R, T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("expected a contiguous float32 lse [R, T, Hq]")
+    status = new_status(dev) if status is None else status
+    ws = workspace(OP_TREE_ATTENTION, R, T, Hq * D, c.heads, dev) if ws is None else ws
+    wp, wn = _ws(ws)
+    scale = D ** -0.5 if scale is None else scale
+    _check(lib().dspark_tree_attention(_p(q), _node_rows(q, k_cache.dtype), R, T, Hq, ctypes.byref(c), _i32(ctx_len, R),
+                                       _i32(n_nodes, R), _i32(mask, R, T, (T + 31) // 32), scale, softcap, _p(out),
+                                       _node_rows(out, k_cache.dtype), _p(lse), wp, wn, _p(status), _stream(stream)),
+           "dspark_tree_attention")
+    return out, lse, status
+
+
+def dspark_tree_accept(tokens, parent, best, *, n_nodes=None, out=None, status=None, stream=None):
+    """Greedy acceptance along a tree: node tokens, parents (None: chains) and the target's choice after each
+    node, all [R, T] int32 -> (out_tokens [R, T], n_accepted [R], path [R, T], status)."""
+    R, T = tokens.shape
+    dev = tokens.device
+    if out is None:
+        out = tuple(torch.empty(z, dtype=torch.int32, device=dev) for z in ((R, T), (R,), (R, T)))
+    status = new_status(dev) if status is None else status
+    _check(lib().dspark_tree_accept(_i32(tokens, R, T), _i32(parent, R, T), _i32(best, R, T), _i32(n_nodes, R), R, T,
+                                    _i32(out[0], R, T), _i32(out[1], R), _i32(out[2], R, T), _p(status),
+                                    _stream(stream)), "dspark_tree_accept")
+    return tuple(out) + (status,)
+
+
+def dspark_cache_commit(k_cache, v_cache, page_table, ctx_len, path, n_accepted, *, T=None, out=None, status=None,
+                        stream=None):
+    """Moves the accepted nodes' rows (path [R, T], n_accepted [R] int32) to the front of their requests'
+    drafted slots, in every layer of k_cache / v_cache ([layers, pages, page, heads, head_dim] or one
+    layer). path None: chains of T nodes, only the length changes. Returns (new_len [R], status)."""
+    c = _kvcache(k_cache, v_cache, page_table)
+    R = page_table.shape[0]
+    if path is not None:
+        T = path.shape[1]
+    out = torch.empty((R,), dtype=torch.int32, device=ctx_len.device) if out is None else out
+    status = new_status(ctx_len.device) if status is None else status
+    _check(lib().dspark_cache_commit(ctypes.byref(c), _i32(ctx_len, R), _i32(path, R, T), _i32(n_accepted, R), R, T,
+                                     _i32(out, R), _p(status), _stream(stream)), "dspark_cache_commit")
+    return out, status

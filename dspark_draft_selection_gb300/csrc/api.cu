@@ -43,14 +43,30 @@ cudaError_t ds_ensure_smem(const void* func, size_t bytes) {
   return e;
 }
 
+DsEncodeFn ds_encode_fn() {
+  static std::once_flag once;
+  static DsEncodeFn fn = nullptr;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<DsEncodeFn>(p);
+    else
+      (void)cudaGetLastError();
+  });
+  return fn;
+}
+
 // Per-op workspace layouts are defined next to their kernels; these sizes must cover them.
 extern "C" size_t dspark_internal_ws_sample(int64_t R, int32_t B, int64_t V);
 extern "C" size_t dspark_internal_ws_dense_walk(int64_t R, int32_t B, int64_t V);
 extern "C" size_t dspark_internal_ws_verify(int64_t R, int32_t B, int64_t V);
 extern "C" size_t dspark_internal_ws_lattice_row(int64_t R, int32_t B, int64_t V);
 
+extern "C" size_t dspark_internal_ws_tree_attention(int64_t R, int32_t T, int64_t cols, int32_t heads);
+
 extern "C" size_t dspark_workspace_size(dspark_op op, int64_t R, int32_t B, int64_t V, int32_t K) {
-  (void)K;
   if (R < 0 || B < 0 || V < 0) return 0;
   switch (op) {
     case DSPARK_OP_D2T_CHECK:
@@ -65,6 +81,8 @@ extern "C" size_t dspark_workspace_size(dspark_op op, int64_t R, int32_t B, int6
       return dspark_internal_ws_verify(R, B, V);
     case DSPARK_OP_LATTICE_ROW:
       return dspark_internal_ws_lattice_row(R, B, V);
+    case DSPARK_OP_TREE_ATTENTION:
+      return dspark_internal_ws_tree_attention(R, B, V, K);
     default:
       return 0;
   }

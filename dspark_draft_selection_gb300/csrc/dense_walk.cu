@@ -608,28 +608,9 @@ __global__ void dense_walk_greedy_kernel(const DwDraw d, int32_t R) {
   dd_emit(d, r, pick, zmax, 1.0, 1.0f, pick);
 }
 
-// cuTensorMapEncodeTiled, from the driver through the runtime (no link against the driver library)
-using DwEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-DwEncodeFn dw_encode_fn() {
-  static std::once_flag once;
-  static DwEncodeFn fn = nullptr;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<DwEncodeFn>(p);
-    else
-      (void)cudaGetLastError();
-  });
-  return fn;
-}
-
 // Tensor map of W [V_t, rank] bf16 for stage loads: box 64 elements (128 bytes) x 128 rows.
 bool dw_tensor_map(CUtensorMap* m, const void* W, int64_t V_t, int rank) {
-  const DwEncodeFn fn = dw_encode_fn();
+  const DsEncodeFn fn = ds_encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {cuuint64_t(rank), cuuint64_t(V_t)};
   const cuuint64_t strides[1] = {cuuint64_t(rank) * 2};

@@ -1,6 +1,7 @@
 // host_common.h - argument checks and launch helpers for the libdspark entry points.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -48,6 +49,13 @@ int ds_num_sms();
 // process driving several GPUs, or calling from several threads, configures each one it uses.
 cudaError_t ds_ensure_smem(const void* func, size_t bytes);
 
+// cuTensorMapEncodeTiled, from the driver through the runtime (no link against the driver library);
+// null when the driver has none.
+using DsEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+DsEncodeFn ds_encode_fn();
+
 // Launches `kern` on `stream` with programmatic stream serialization: it may start while the
 // previous kernel on the stream is still running (see ds_pdl_trigger / ds_pdl_wait).
 template <typename... KArgs, typename... Args>
@@ -64,4 +72,21 @@ static inline cudaError_t ds_launch(void (*kern)(KArgs...), dim3 grid, dim3 bloc
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// Checks of a dspark_kvcache that every cache entry point makes (`layers`: the layer count is used).
+static inline bool ds_cache_ok(const dspark_kvcache* c, bool layers) {
+  if (!c || !c->k || !c->v || !c->page_table || !ds_dtype_ok(c->dtype)) return false;
+  const size_t e = size_t(ds_dtype_size(c->dtype));
+  return ds_aligned(c->k, e) && ds_aligned(c->v, e) && c->page_stride >= 0 && c->token_stride >= 0 &&
+         c->head_stride >= 0 && c->num_pages >= 1 && c->num_pages <= INT32_MAX && c->page_size >= 1 &&
+         c->page_size <= 65536 && c->heads >= 1 && c->heads <= 1024 && c->head_dim >= 8 && c->head_dim <= 256 &&
+         c->head_dim % 8 == 0 && c->table_pages >= 1 && c->ld_table >= c->table_pages && (!layers || (c->n_layers >= 1 && c->layer_stride >= 0));
+}
+
+// Every row of every head of the cache starts on a 16-byte boundary.
+static inline bool ds_cache_vec(const dspark_kvcache* c) {
+  const int64_t e = ds_dtype_size(c->dtype);
+  return ds_aligned(c->k, 16) && ds_aligned(c->v, 16) && (c->page_stride * e) % 16 == 0 &&
+         (c->token_stride * e) % 16 == 0 && (c->head_stride * e) % 16 == 0 && (c->layer_stride * e) % 16 == 0;
 }

@@ -1,0 +1,177 @@
+// tree_attn.cuh - what the kernels of dspark_tree_attention share: arguments, the split of the work
+// over the blocks and the layout of the partial results.
+#pragma once
+
+#include "dspark_common.cuh"
+#include "host_common.h"
+
+constexpr int TA_MAXR = 1024;
+constexpr int TA_MAXT = 512;
+
+struct TaArgs {
+  const void* q;
+  int64_t ldq;
+  void* out;
+  int64_t ldo;
+  float* lse;
+  dspark_kvcache c;
+  const int32_t *ctx_len, *n_nodes;
+  const uint32_t* mask;
+  int32_t R, T, Hq, G, W;      // G query heads per key head, W mask words per node
+  int32_t rows;                // T * G query rows per (request, key head); row m is node m / G, head m % G
+  int32_t rpg, mg;             // rows per row group, row groups
+  int32_t rs;                  // row stride of a partial result, >= the rows of a group that exist
+  int32_t kt;                  // keys per tile
+  int32_t box;                 // keys per copy (tensor-core kernel)
+  float scale, softcap;
+  int32_t* pref;               // [R + 1] running sum of the requests' tile counts
+  float2* part_ml;             // [slots][rs] (reference maximum in log2 units, sum)
+  float4* part_o;              // [slots][D / 4][rs] sums of weights times values, relative to the maximum
+  int32_t* status;
+  uint32_t first_wait;
+};
+
+// The work is a line of tiles: requests in order, in each its (key head, row group) items in order,
+// in each item its key tiles in order (at least one, so that empty requests get their zeros written).
+// Block b of `grid` takes tiles [total b / grid, total (b + 1) / grid): every block has the same
+// number of tiles (+-1) whatever the lengths, which only the device knows. An item that a block holds
+// whole is finished there; of the others each block leaves a partial result - slot 2 b for one that an
+// earlier block began, 2 b + 1 for one that it began itself - and the combine kernel joins them in
+// the order of the blocks.
+struct TaPiece {
+  int32_t r, hk, g;            // request, key head, row group
+  int32_t t0, t1, nt;          // tiles [t0, t1) of the item's nt
+  DS_DEV bool whole() const { return t0 == 0 && t1 == nt; }
+  DS_DEV int64_t slot(int64_t b) const { return 2 * b + (t0 > 0 ? 0 : 1); }
+};
+
+struct TaWalk {
+  int64_t at, end;
+  int32_t r;
+  DS_DEV void init(const int32_t* pref, const TaArgs& a, int64_t b, int64_t grid) {
+    const int64_t hm = int64_t(a.c.heads) * a.mg, total = int64_t(pref[a.R]) * hm;
+    at = total * b / grid;
+    end = total * (b + 1) / grid;
+    int lo = 0, hi = a.R;      // the last request that begins at or before `at`
+    while (lo + 1 < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (int64_t(pref[mid]) * hm <= at) lo = mid;
+      else hi = mid;
+    }
+    r = lo;
+  }
+  DS_DEV bool next(const int32_t* pref, const TaArgs& a, TaPiece& p) {
+    if (at >= end) return false;
+    const int64_t hm = int64_t(a.c.heads) * a.mg;
+    while (int64_t(pref[r + 1]) * hm <= at) ++r;
+    const int64_t off = at - int64_t(pref[r]) * hm;
+    p.r = r;
+    p.nt = pref[r + 1] - pref[r];
+    const int32_t item = int32_t(off / p.nt);
+    p.t0 = int32_t(off - int64_t(item) * p.nt);
+    p.t1 = int32_t(min(int64_t(p.nt), p.t0 + (end - at)));
+    p.hk = item / a.mg;
+    p.g = item - p.hk * a.mg;
+    at += p.t1 - p.t0;
+    return true;
+  }
+};
+
+// Committed length and node count of request r; what is out of range is reported and cut so that no
+// slot past the page table is read.
+DS_DEV void ta_lens(const TaArgs& a, int r, int32_t& ctx, int32_t& n) {
+  ctx = a.ctx_len[r];
+  n = a.n_nodes ? a.n_nodes[r] : a.T;
+  if (n < 0 || n > a.T || ctx < 0) {
+    ds_set_error(a.status, DSPARK_EINVAL);
+    n = 0;
+    ctx = max(ctx, 0);
+  }
+  const int64_t cap = int64_t(a.c.table_pages) * a.c.page_size;
+  if (int64_t(ctx) + n > cap) {
+    ds_set_error(a.status, DSPARK_ERANGE);
+    ctx = int32_t(min(int64_t(ctx), cap));
+    n = int32_t(min(int64_t(n), cap - ctx));
+  }
+}
+
+// pref[0..R] in shared memory, by all threads of the block.
+DS_DEV void ta_prefix(const TaArgs& a, int32_t* pref) {
+  for (int r = threadIdx.x; r < a.R; r += blockDim.x) {
+    int32_t ctx, n;
+    ta_lens(a, r, ctx, n);
+    pref[r + 1] = max(1, int32_t((int64_t(ctx) + n + a.kt - 1) / a.kt));
+  }
+  if (threadIdx.x == 0) pref[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int32_t run = 0;
+    for (int r0 = 0; r0 < a.R; r0 += 32) {
+      const int r = r0 + int(threadIdx.x);
+      int32_t v = r < a.R ? pref[r + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t up = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (int(threadIdx.x) >= d) v += up;
+      }
+      v += run;
+      if (r < a.R) pref[r + 1] = v;
+      run = __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+  }
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int r = threadIdx.x; r <= a.R; r += blockDim.x) a.pref[r] = pref[r];
+}
+
+// Bits of the 32 keys whose first is node `nd` (negative: committed slots, which every node sees),
+// as node i of n sees them.
+DS_DEV uint32_t ta_mask32(const TaArgs& a, int r, int i, int n, int64_t nd) {
+  if (nd <= -32) return 0xFFFFFFFFu;
+  const int lim = a.mask ? n : min(n, i + 1);        // without a mask node i sees nodes j <= i
+  if (nd >= lim) return 0u;
+  uint32_t bits = 0xFFFFFFFFu;
+  if (a.mask) {
+    const uint32_t* row = a.mask + (int64_t(r) * a.T + i) * a.W;
+    if (nd < 0) {
+      bits = (row[0] << uint32_t(-nd)) | ((1u << uint32_t(-nd)) - 1u);
+    } else {
+      const int w = int(nd >> 5);
+      const uint32_t lo = row[w], hi = w + 1 < a.W ? row[w + 1] : 0u;
+      bits = __funnelshift_r(lo, hi, uint32_t(nd) & 31u);
+    }
+  }
+  const int64_t left = lim - nd;                     // keys of these 32 that exist
+  return left >= 32 ? bits : bits & ((1u << left) - 1u);
+}
+
+// Element offset of slot s of request r, or -1.
+DS_DEV int64_t ta_slot(const TaArgs& a, int r, int64_t s) {
+  const int64_t e = s / a.c.page_size;
+  if (e >= a.c.table_pages) return -1;
+  const int32_t p = a.c.page_table[int64_t(r) * a.c.ld_table + e];
+  if (p < 0 || p >= a.c.num_pages) {
+    ds_set_error(a.status, DSPARK_ERANGE);
+    return -1;
+  }
+  return int64_t(p) * a.c.page_stride + (s - e * a.c.page_size) * a.c.token_stride;
+}
+
+DS_DEV float ta_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// cap * tanh(x) with tanh(x) = 1 - 2 / (1 + e^(2 x)); `x2` is 2 x log2(e). Its error, about 2^-22 of the
+// cap whatever x, is far below what a tanh instruction leaves (about 2^-11).
+DS_DEV float ta_tanh(float x2, float cap) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ta_ex2(x2)));
+  return __fmaf_rn(-2.0f * cap, r, cap);
+}
+
+constexpr float TA_LOG2E = 1.4426950408889634f;
+constexpr float TA_LN2 = 0.6931471805599453f;
+
+// Join of the partial results and the launch of it (tree_attn.cu).
+cudaError_t ta_launch_float(const TaArgs& a, int grid, cudaStream_t st);

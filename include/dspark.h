@@ -82,7 +82,8 @@ typedef enum {
   DSPARK_OP_DENSE_WALK = 4,
   DSPARK_OP_VERIFY = 5,
   DSPARK_OP_D2T_CHECK = 6,
-  DSPARK_OP_LATTICE_ROW = 7
+  DSPARK_OP_LATTICE_ROW = 7,
+  DSPARK_OP_TREE_ATTENTION = 8
 } dspark_op;
 
 /*
@@ -396,6 +397,120 @@ dspark_status dspark_lattice_row_sample(const void* logits, dspark_dtype dtype, 
 dspark_status dspark_grouped_conv(const void* x, dspark_dtype dtype, int64_t N, int64_t C, int64_t ldx,
                                   int32_t G, int32_t L, const float* k, const int32_t* block, float* y,
                                   int64_t ldy, dspark_stream_t stream);
+
+/*
+ * One verification step of drafted nodes over a paged key/value cache: the target model's side
+ * between drafting and dspark_verify, for chains (a drafted block) and trees (a block with
+ * alternatives from the Top-K candidates). The pages run it inside the target model with paged
+ * attention and give no formulas; the definitions are these.
+ *
+ * R requests have T node slots each and n_r = n_nodes[r] nodes (int32 device array, 0..T; NULL: T
+ * everywhere; another value sets DSPARK_EINVAL on *dev_status and counts as 0). parent [R, T] int32
+ * device: a node's parent has a lower index, -1 is a node that follows the committed tokens
+ * directly (a root); NULL is the chain parent[i] = i - 1. Request r has ctx_len[r] >= 0 (int32
+ * device) committed tokens in its cache, and node i belongs in slot ctx_len[r] + i.
+ *
+ * The cache: keys and values are two buffers of `dtype` with one layout, element (page p, place t,
+ * head h, column d) of layer l at l * layer_stride + p * page_stride + t * token_stride +
+ * h * head_stride + d (strides in elements, >= 0). Slot s of request r is place s % page_size of
+ * page page_table[r * ld_table + s / page_size] (int32 device, ids 0..num_pages - 1; table_pages
+ * entries to a row). A slot past the table's row, or a page id out of range, sets DSPARK_ERANGE on *dev_status: nothing is written
+ * there, and attention reads zeros. page_size 1..65536, heads >= 1, head_dim a multiple of 8,
+ * 8..256.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  dspark_dtype dtype;
+  int32_t n_layers; /* dspark_cache_commit treats every layer; the others use the first */
+  int64_t layer_stride, page_stride, token_stride, head_stride;
+  int64_t num_pages;
+  int32_t page_size, heads, head_dim;
+  const int32_t* page_table;
+  int32_t ld_table, table_pages; /* row stride of the table, entries of a row (table_pages <= ld_table) */
+} dspark_kvcache;
+
+/*
+ * Ancestor mask and positions of drafted trees. Bit j of mask[r, i, :] (word j / 32, bit j % 32) is
+ * 1 when node j is node i or one of its ancestors; pos[r, i] = base[r] + the number of i's ancestors
+ * (base [R] int32 device: position of the first node after the committed tokens; NULL: 0). Node
+ * slots i >= n_r get an empty mask and position 0. A parent that is not before its node (or < -1)
+ * sets DSPARK_EINVAL on *dev_status and makes the node a root. T 1..512; W = (T + 31) / 32 words.
+ * mask [R, T, W] uint32, pos [R, T] int32, device.
+ */
+dspark_status dspark_tree_mask(const int32_t* parent, const int32_t* n_nodes, const int32_t* base,
+                               int64_t R, int32_t T, uint32_t* mask, int32_t* pos,
+                               int32_t* dev_status, dspark_stream_t stream);
+
+/*
+ * Rotary positions and append. Rows are node slots (r, i) = r * T + i: q [R * T, ldq], heads Hq side
+ * by side (Hq a multiple of cache->heads); k and v [R * T, ldk / ldv] with cache->heads heads; all of
+ * cache->dtype and cache->head_dim columns a head. The first `rot` columns of every q and k head
+ * (even, <= head_dim) turn in rot / 2 pairs: pair f is columns (f, f + rot / 2), or (2 f, 2 f + 1)
+ * when interleaved != 0, and (x1, x2) becomes (x1 c - x2 s, x2 c + x1 s), computed in float32 and
+ * rounded once, with c = cos_sin[p, f], s = cos_sin[p, rot / 2 + f] of the float32 table
+ * cos_sin [P, rot] (device), p = pos[(r * T + i) * A + axis[f]]. A (1..8) position axes - several
+ * for images and video (time, height, width) - and axis [rot / 2] int32 (device; NULL: axis 0).
+ * Turned queries go to q_out [R * T, ldo] (may be q itself with ldo = ldq; zero for i >= n_r), turned
+ * keys and the values to the nodes' cache slots. A position outside 0..P - 1 or an axis outside
+ * 0..A - 1 sets DSPARK_ERANGE on *dev_status and turns as position 0 / axis 0. T >= 1 (any length:
+ * a prompt's rows are a chain too). Cache slots may not be shared between rows.
+ */
+dspark_status dspark_rope_append(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                 const void* v, int64_t ldv, int64_t R, int32_t T, int32_t Hq,
+                                 const int32_t* pos, int32_t A, const float* cos_sin, int64_t P,
+                                 int32_t rot, const int32_t* axis, int32_t interleaved,
+                                 const dspark_kvcache* cache, const int32_t* ctx_len,
+                                 const int32_t* n_nodes, void* q_out, int64_t ldo,
+                                 int32_t* dev_status, dspark_stream_t stream);
+
+/*
+ * Attention of the nodes over the cache. q and out: [R * T, ldq / ldo] of cache->dtype, Hq heads of
+ * head_dim columns side by side; query head h reads key head h / (Hq / heads). Node i sees every
+ * committed slot and the slots of the nodes whose bit is set in its mask row (mask [R, T, W] as
+ * dspark_tree_mask writes it, any pattern allowed - a whole block, a prefix; NULL: nodes j <= i).
+ *   x = scale q . k; softcap > 0: x = softcap tanh(x / softcap); p = softmax of x over what i sees;
+ *   out = sum p v; lse (nullable) [R, T, Hq] float32 = log of the sum of exp x.
+ * A row that sees nothing, and slots i >= n_r, give zeros and lse = -inf. What a row does not see has
+ * no effect on it, infinities and NaN included. Sums and statistics are float32; with bf16 the
+ * products run on the tensor cores and the weights p are rounded to bf16 for the product with v
+ * (bf16 caches with head_dim <= 128, page_size % 8 == 0 and 16-byte aligned rows; others in float32).
+ * scale > 0, softcap >= 0 finite. R <= 1024, T 1..512, Hq <= 1024. The result does not depend on
+ * the run: no atomics. ws: dspark_workspace_size(DSPARK_OP_TREE_ATTENTION, R, T, Hq * head_dim,
+ * heads) bytes.
+ */
+dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64_t R, int32_t T, int32_t Hq,
+                                    const dspark_kvcache* cache, const int32_t* ctx_len,
+                                    const int32_t* n_nodes, const uint32_t* mask, float scale,
+                                    float softcap, void* out, int64_t ldo, float* lse, void* ws,
+                                    size_t ws_bytes, int32_t* dev_status, dspark_stream_t stream);
+
+/*
+ * Greedy acceptance along a tree. tokens [R, T] int32: node tokens (node 0 is the last verified
+ * token); best [R, T] int32: the target's choice after each node (dspark_topk with K = 1 on the
+ * target's rows). From node 0, the walk goes to the lowest-indexed child whose token is the choice
+ * at the node it is on, until there is none. out_tokens [R, T] int32: the accepted tokens, then the
+ * choice at the last node (the correction or bonus), then -1; n_accepted [R] int32: nodes accepted
+ * after node 0; path [R, T] int32: node 0 and the accepted nodes, then -1. n_r = 0 gives
+ * n_accepted = -1 and -1 everywhere. Nodes whose parent is not before them are never reached.
+ * T 1..512.
+ */
+dspark_status dspark_tree_accept(const int32_t* tokens, const int32_t* parent, const int32_t* best,
+                                 const int32_t* n_nodes, int64_t R, int32_t T, int32_t* out_tokens,
+                                 int32_t* n_accepted, int32_t* path, int32_t* dev_status,
+                                 dspark_stream_t stream);
+
+/*
+ * Keeps the accepted nodes: for k = 0..n_accepted[r], in every layer, slot ctx_len[r] + path[r, k]
+ * of the keys and values moves to slot ctx_len[r] + k, and new_len[r] = ctx_len[r] + n_accepted[r]
+ * + 1 (new_len [R] int32 device, not ctx_len itself). path [R, T] int32 ascending, as
+ * dspark_tree_accept writes it; NULL: a chain, nothing moves. n_accepted < 0: nothing moves and the
+ * length stays. n_accepted >= T, or a path entry that is not above the one before and below T, sets
+ * DSPARK_EINVAL on *dev_status and leaves that request as it was. T 1..512, R <= 65535.
+ */
+dspark_status dspark_cache_commit(const dspark_kvcache* cache, const int32_t* ctx_len,
+                                  const int32_t* path, const int32_t* n_accepted, int64_t R, int32_t T,
+                                  int32_t* new_len, int32_t* dev_status, dspark_stream_t stream);
 
 /*
  * Failure-detection test hook (not part of the method): sets the poll limit of the first wait

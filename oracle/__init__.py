@@ -24,7 +24,10 @@ Modules and what pins them (the tests under ``tests/test_oracle_*.py``):
             and greedy acceptance equal to argmax matching);
   conv      DFlash-2 grouped dynamic convolution over packed block rows (pinned by one tap
             equal to a per-group scaling, one block with fixed taps equal to numpy's causal
-            convolution of every channel, block isolation under perturbation, linearity).
+            convolution of every channel, block isolation under perturbation, linearity);
+  tree      drafted trees over a cache: mask, rotary positions, attention, acceptance, commit
+            (pinned by matrix powers, rotations' lengths and differences of positions, each
+            node equal to the chain that leads to it, enumeration of all paths).
 No function here is "parity unpinned".
 """
-from . import conv, draft, fp32, philox, sampling, verify, walk  # noqa: F401
+from . import conv, draft, fp32, philox, sampling, tree, verify, walk  # noqa: F401
