@@ -124,8 +124,9 @@ def _dt(t) -> int:
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())   # no Stream object for every call
 
 
 def _rows(t):
@@ -450,7 +451,7 @@ def _i32(t, *shape):
     """Pointer of a contiguous int32 device tensor of this shape (None: no tensor)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"expected a contiguous int32 tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
     return _p(t)
 

@@ -50,15 +50,91 @@ DS_DEV void ta_tma_load(void* dst, const void* tmap, int32_t d, int32_t t, int32
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], kind::f16; one thread.
+// The MMA warp stays together, so that descriptors and addresses are uniform registers, and one elected
+// lane - the same one every time - issues: D[tmem] (+)= A[smem] * B[smem], kind::f16,
+DS_DEV void ta_umma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem],
 DS_DEV void ta_umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// and the arrival on an mbarrier once everything issued before is complete.
+DS_DEV void ta_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ds_smem_addr(bar))
+      : "memory");
+}
+
+// 32 columns of tensor memory on their way into registers; ta_arrived waits for all that are.
+DS_DEV void ta_tmem_fetch(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+DS_DEV void ta_arrived(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                 "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                 "+f"(v[30]), "+f"(v[31])::"memory");
+}
+
+DS_DEV void ta_tmem_fetch(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr));
+}
+DS_DEV void ta_arrived(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                 "+f"(v[15])::"memory");
+}
+
+// cap2 * tanh(sy * s) = s * Q(s^2) for |sy * s| <= 1: tanh(y) = y P(y^2) with the seven coefficients of P
+// that make the largest relative error smallest (5e-8, fitted by reweighted least squares; 1.6e-7 as
+// evaluated in float32), scaled by the powers of sy and by cap2; two values at a time.
+struct TaTanhPoly {
+  float c[7];
+  DS_DEV TaTanhPoly(float sy, float cap2) {
+    const float p[7] = {0x1.fffffep-1f, -0x1.55540ap-2f, 0x1.10e672p-3f, -0x1.b5eb8p-5f, 0x1.4c6e4ap-6f, -0x1.968b3ap-8f, 0x1.10e592p-10f};
+    float f = sy * cap2;
+#pragma unroll
+    for (int k = 0; k < 7; ++k, f *= sy * sy) c[k] = p[k] * f;
+  }
+  DS_DEV uint64_t at(uint64_t s) const {
+    const uint64_t u = ds_fma2(s, s, 0);
+    uint64_t q = ds_f2(c[6], c[6]);
+#pragma unroll
+    for (int k = 5; k >= 0; --k) q = ds_fma2(q, u, ds_f2(c[k], c[k]));
+    return q;
+  }
+};
 
 // Descriptor of an operand whose N index is contiguous (V: rows are keys, 64 columns of D to a
 // 128-byte row): 64-column blocks lie TA_CHUNK apart, groups of eight keys 1024 bytes apart.
@@ -72,6 +148,11 @@ DS_DEV uint64_t ta_desc_nmajor(uint32_t saddr) {
   return d;
 }
 
+DS_DEV void ta_tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 DS_DEV void ta_tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -92,11 +173,10 @@ DS_DEV uint32_t ta_pack(float lo, float hi) {
 // not finite where drafted nodes are among the keys. The product P V adds 0 * v for a node that the
 // row does not see, and that is not a number when v is not finite; here such a node is passed over.
 // One warp per row; writes columns [d0, d1) relative to the reference maximum `mref`, times `mul`.
-__device__ __noinline__ void ta_row_again(const TaArgs& a, int r, int hk, int m, int64_t k0, int64_t k1, float mref,
-                                          float mul, int d0, int d1, __nv_bfloat16* out, float4* part) {
+__device__ __noinline__ void ta_row_again(const TaArgs& a, int r, int32_t ctx, int32_t n, int hk, int m, int64_t k0,
+                                          int64_t k1, float mref, float mul, int d0, int d1, __nv_bfloat16* out,
+                                          float* part) {
   const int lane = threadIdx.x & 31;
-  int32_t ctx, n;
-  ta_lens(a, r, ctx, n);
   const int i = m / a.G, h = hk * a.G + m % a.G, D = a.c.head_dim;
   const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t(r) * a.T + i) * a.ldq + int64_t(h) * D;
   const __nv_bfloat16* kc = reinterpret_cast<const __nv_bfloat16*>(a.c.k) + hk * a.c.head_stride;
@@ -124,7 +204,7 @@ __device__ __noinline__ void ta_row_again(const TaArgs& a, int r, int hk, int m,
     const int d = d0 + lane + 32 * u;
     if (d >= d1) continue;
     if (out) out[d] = __float2bfloat16_rn(acc[u] * mul);
-    else reinterpret_cast<float*>(part + int64_t(d >> 2) * a.rs)[d & 3] = acc[u];
+    else part[d] = acc[u];
   }
 }
 
@@ -140,10 +220,10 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
   __shared__ uint64_t s_full[NS], s_empty[NS], s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_ofull, s_ofree, s_mlfull, s_drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ int32_t s_pref[TA_MAXR + 1];
+  __shared__ TaLens s_len;
   __shared__ float2 s_ml[2][2][128];                   // [piece parity][group][row]
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sR = sQ + (TWO ? 2 : 1) * STAGE;            // the ring (a query tile has a stage's size)
 
@@ -169,9 +249,9 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
   ds_pdl_wait();
   if (warp == 1) ds_tmem_alloc(&s_tmem, 512);
   ds_tc_fence_before();
-  ta_prefix(a, s_pref);                                // synchronises the block
+  ta_prefix(a, s_len);                                // synchronises the block
   ds_tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
   auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t limit) {
     if (!ds_mbar_wait_or_abort(bar, parity & 1u, limit, &s_abort)) {
@@ -181,7 +261,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     return !aborted();
   };
   TaWalk walk;
-  walk.init(s_pref, a, blockIdx.x, gridDim.x);
+  walk.init(s_len, a, blockIdx.x, gridDim.x);
   TaPiece p;
 
   if (warp == 0) {
@@ -190,9 +270,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     const int box = a.box, nbox = TA_KT / box;
     uint32_t seq = 0;
     bool ok = true;
-    while (ok && walk.next(s_pref, a, p)) {
-      int32_t ctx, n;
-      ta_lens(a, p.r, ctx, n);
+    while (ok && walk.next(s_len, a, p)) {
+      const int32_t ctx = s_len.ctx[p.r], n = s_len.n[p.r];
       const int64_t len = int64_t(ctx) + n;
       const int32_t* table = a.c.page_table + int64_t(p.r) * a.c.ld_table;
       int32_t place = 0;
@@ -244,116 +323,117 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
         (void)ds_mbar_wait(&s_full[k % NS], (k / NS) & 1u, DS_WAIT_LIMIT);
     __syncwarp();
   } else if (warp == 1) {
-    // ---- one thread issues the MMAs. QK of a group's next tile follows the group's PV: S and P share
+    // ---- one lane issues the MMAs. QK of a group's next tile follows the group's PV: S and P share
     // tensor memory, and the MMAs of one thread run in order ----
-    if (lane == 0) {
-      constexpr uint32_t idS = ds_idesc_bf16_f32(128, TA_KT);
-      constexpr uint32_t idO = ds_idesc_bf16_f32(128, DP) | (1u << 16);   // B is N-major
-      const uint32_t qaddr = ds_smem_addr(sQ), raddr = ds_smem_addr(sR);
-      uint32_t seq = 0, np = 0, pn[2] = {0, 0};
-      bool ok = true;
-      auto full = [&](uint32_t sq) {
-        ok = ok && wait(&s_full[sq % NS], sq / NS, DS_WAIT_LIMIT);
-        ds_tc_fence_after();
-        return ok;
-      };
-      auto release = [&](uint32_t sq) { ds_umma_commit(&s_empty[sq % NS]); };
-      auto qk = [&](int g, uint32_t sq) {
-        const uint32_t q0 = qaddr + (TWO ? g : 0) * STAGE, k0 = raddr + (sq % NS) * STAGE;
+    constexpr uint32_t idS = ds_idesc_bf16_f32(128, TA_KT);
+    constexpr uint32_t idO = ds_idesc_bf16_f32(128, DP) | (1u << 16);   // B is N-major
+    // addresses stay below 2^18, so a descriptor's address field (in 16 bytes) takes plain additions
+    const uint64_t qdesc = ds_smem_desc_sw128(ds_smem_addr(sQ)), kdesc = ds_smem_desc_sw128(ds_smem_addr(sR)),
+                   vdesc = ta_desc_nmajor(ds_smem_addr(sR));
+    uint32_t seq = 0, np = 0, pn[2] = {0, 0};
+    bool ok = true;
+    auto full = [&](uint32_t sq) {
+      ok = ok && wait(&s_full[sq % NS], sq / NS, DS_WAIT_LIMIT);
+      ds_tc_fence_after();
+      return ok;
+    };
+    auto release = [&](uint32_t sq) { ta_commit(&s_empty[sq % NS]); };
+    auto qk = [&](int g, uint32_t sq) {
+      const uint64_t q0 = qdesc + (((TWO ? g : 0) * STAGE) >> 4), k0 = kdesc + (((sq % NS) * STAGE) >> 4);
 #pragma unroll
-        for (int kb = 0; kb < DP / 16; ++kb) {
-          const uint32_t off = (kb >> 2) * TA_CHUNK + (kb & 3) * 32;
-          ds_umma_f16(tmem + TS + 128 * g, ds_smem_desc_sw128(q0 + off), ds_smem_desc_sw128(k0 + off), idS, kb != 0);
-        }
-        ds_umma_commit(&s_sfull[g]);
-      };
-      auto pv = [&](int g, uint32_t sq, bool acc) {
-        const uint32_t v0 = raddr + (sq % NS) * STAGE;
-#pragma unroll
-        for (int kb = 0; kb < TA_KT / 16; ++kb)
-          ta_umma_ts(tmem + TO + DP * g, tmem + TS + 128 * g + kb * 8, ta_desc_nmajor(v0 + kb * 2048), idO, acc || kb != 0);
-      };
-      auto weights = [&](int g, bool first) {          // P of group g is written; at first O must be free too
-        ok = ok && wait(&s_pfull[g], pn[g]++, DS_WAIT_LIMIT);
-        if (first && np > 0) ok = ok && wait(&s_ofree, np - 1, DS_WAIT_LIMIT);
-        ds_tc_fence_after();
-        return ok;
-      };
-      while (ok && walk.next(s_pref, a, p)) {
-        const int nt = p.t1 - p.t0;
-        ok = wait(&s_qfull, np, DS_WAIT_LIMIT);
-        if (!ok) break;
-        ds_tc_fence_after();
-        if (TWO) {                                     // ring order: K0, then V_t, K_{t+1}
-          if (!full(seq)) break;
-          qk(0, seq);
-          qk(1, seq);
-          release(seq++);
-          if (nt == 1) ds_umma_commit(&s_qempty);
-          for (int t = 0; t < nt; ++t) {
-            const bool more = t + 1 < nt;
-            if (!weights(0, t == 0) || !full(seq)) break;
-            pv(0, seq, t > 0);
-            if (more) {
-              if (!full(seq + 1)) break;
-              qk(0, seq + 1);
-            }
-            if (!weights(1, false)) break;
-            pv(1, seq, t > 0);
-            release(seq++);
-            if (more) {
-              qk(1, seq);
-              release(seq++);
-              if (t + 2 == nt) ds_umma_commit(&s_qempty);
-            }
-          }
-        } else {                                       // ring order: K0, K1, then V_t, K_{t+2}
-          for (int t = 0; t < min(2, nt); ++t) {
-            if (!full(seq)) break;
-            qk(t, seq);
-            release(seq++);
-          }
-          if (nt <= 2) ds_umma_commit(&s_qempty);
-          for (int t = 0; ok && t < nt; ++t) {
-            const int g = t & 1;
-            if (!weights(g, t == 0) || !full(seq)) break;
-            pv(g, seq, t >= 2);
-            release(seq++);
-            if (t + 2 < nt) {
-              if (!full(seq)) break;
-              qk(g, seq);
-              release(seq++);
-              if (t + 3 == nt) ds_umma_commit(&s_qempty);
-            }
-          }
-        }
-        if (!ok) break;
-        ds_umma_commit(&s_ofull);
-        ++np;
+      for (int kb = 0; kb < DP / 16; ++kb) {
+        const uint32_t off = ((kb >> 2) * TA_CHUNK + (kb & 3) * 32) >> 4;
+        ta_umma_ss(tmem + TS + 128 * g, q0 + off, k0 + off, idS, kb != 0);
       }
-      ds_umma_commit(&s_drain);                        // the MMAs are done before tensor memory goes
-      (void)ds_mbar_wait(&s_drain, 0, DS_WAIT_LIMIT);
+      ta_commit(&s_sfull[g]);
+    };
+    auto pv = [&](int g, uint32_t sq, bool acc) {
+      const uint64_t v0 = vdesc + (((sq % NS) * STAGE) >> 4);
+#pragma unroll
+      for (int kb = 0; kb < TA_KT / 16; ++kb)
+        ta_umma_ts(tmem + TO + DP * g, tmem + TS + 128 * g + kb * 8, v0 + ((kb * 2048) >> 4), idO, acc || kb != 0);
+    };
+    auto weights = [&](int g, bool first) {          // P of group g is written; at first O must be free too
+      ok = ok && wait(&s_pfull[g], pn[g]++, DS_WAIT_LIMIT);
+      if (first && np > 0) ok = ok && wait(&s_ofree, np - 1, DS_WAIT_LIMIT);
+      ds_tc_fence_after();
+      return ok;
+    };
+    while (ok && walk.next(s_len, a, p)) {
+      const int nt = p.t1 - p.t0;
+      ok = wait(&s_qfull, np, DS_WAIT_LIMIT);
+      if (!ok) break;
+      ds_tc_fence_after();
+      if (TWO) {                                     // ring order: K0, then V_t, K_{t+1}
+        if (!full(seq)) break;
+        qk(0, seq);
+        qk(1, seq);
+        release(seq++);
+        if (nt == 1) ta_commit(&s_qempty);
+        for (int t = 0; t < nt; ++t) {
+          const bool more = t + 1 < nt;
+          if (!weights(0, t == 0) || !full(seq)) break;
+          pv(0, seq, t > 0);
+          if (more) {
+            if (!full(seq + 1)) break;
+            qk(0, seq + 1);
+          }
+          if (!weights(1, false)) break;
+          pv(1, seq, t > 0);
+          release(seq++);
+          if (more) {
+            qk(1, seq);
+            release(seq++);
+            if (t + 2 == nt) ta_commit(&s_qempty);
+          }
+        }
+      } else {                                       // ring order: K0, K1, then V_t, K_{t+2}
+        for (int t = 0; t < min(2, nt); ++t) {
+          if (!full(seq)) break;
+          qk(t, seq);
+          release(seq++);
+        }
+        if (nt <= 2) ta_commit(&s_qempty);
+        for (int t = 0; ok && t < nt; ++t) {
+          const int g = t & 1;
+          if (!weights(g, t == 0) || !full(seq)) break;
+          pv(g, seq, t >= 2);
+          release(seq++);
+          if (t + 2 < nt) {
+            if (!full(seq)) break;
+            qk(g, seq);
+            release(seq++);
+            if (t + 3 == nt) ta_commit(&s_qempty);
+          }
+        }
+      }
+      if (!ok) break;
+      ta_commit(&s_ofull);
+      ++np;
     }
-    __syncwarp();
+    ta_commit(&s_drain);                        // the MMAs are done before tensor memory goes
+    (void)ds_mbar_wait(&s_drain, 0, DS_WAIT_LIMIT);
   } else if (warp < 4) {
     // ---- query rows of each piece into the swizzled layout; columns past head_dim are zero (the key
     // tile's are too), rows that do not exist keep what was there: a row only reaches its own results ----
-    const int qt = tid - 64, cpr = DP / 8, D = a.c.head_dim;
+    constexpr int CPR = DP / 8, STEP = TA_QTHREADS / CPR;        // 16-byte columns of a row, rows per round
+    const int qt = tid - 64, c = qt % CPR, D = a.c.head_dim;
     uint32_t np = 0;
-    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q);
-    while (walk.next(s_pref, a, p)) {
+    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + c * 8;
+    uint8_t* dst = sQ + (c >> 3) * TA_CHUNK;
+    while (walk.next(s_len, a, p)) {
       if (np > 0 && !wait(&s_qempty, np - 1, DS_WAIT_LIMIT)) break;
       const int m0 = p.g * a.rpg, cnt = min(a.rpg, a.rows - m0);
-#pragma unroll 4
-      for (int u = qt; u < cnt * cpr; u += TA_QTHREADS) {
-        const int lr = u / cpr, c = u % cpr, m = m0 + lr, i = m / a.G;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (c * 8 < D)
-          x = __ldg(reinterpret_cast<const uint4*>(q + (int64_t(p.r) * a.T + i) * a.ldq +
-                                                   int64_t(p.hk * a.G + (m - i * a.G)) * D + c * 8));
+      int i = (m0 + qt / CPR) / a.G, h = (m0 + qt / CPR) - i * a.G;
+      const __nv_bfloat16* qr = q + int64_t(p.r) * a.T * a.ldq + int64_t(p.hk) * a.G * D;
+      for (int lr = qt / CPR; lr < cnt; lr += STEP) {
         const int row = lr & 127;
-        *reinterpret_cast<uint4*>(sQ + (lr >> 7) * STAGE + (c >> 3) * TA_CHUNK + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x;
+        uint8_t* at = dst + (lr >> 7) * STAGE + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+        if (c * 8 < D) ds_cp_async16(at, qr + int64_t(i) * a.ldq + h * D);
+        else *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+        for (h += STEP; h >= a.G; h -= a.G) ++i;
       }
+      ds_cp_async_wait_all();
       ds_fence_proxy_async_smem();
       ds_mbar_arrive(&s_qfull);
       ++np;
@@ -364,13 +444,13 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     const uint32_t tl = tmem + (uint32_t(quarter * 32) << 16);
     const uint32_t tS = tl + TS + 128 * g, tO = tl + TO + DP * g;
     const float sc = CAP ? a.scale * 2.0f * TA_LOG2E / a.softcap : a.scale * TA_LOG2E;
-    const float cap2 = a.softcap * TA_LOG2E;
+    const float cap2 = a.softcap * TA_LOG2E, sy = CAP ? a.scale / a.softcap : 0.0f;
+    const TaTanhPoly tanh_poly(sy, cap2);
     const int D = a.c.head_dim;
     uint32_t np = 0, ns = 0, seq = 0;
     bool first = true, ok = true;
-    while (ok && walk.next(s_pref, a, p)) {
-      int32_t ctx, n;
-      ta_lens(a, p.r, ctx, n);
+    while (ok && walk.next(s_len, a, p)) {
+      const int32_t ctx = s_len.ctx[p.r], n = s_len.n[p.r];
       const int64_t len = int64_t(ctx) + n;
       const int npt = p.t1 - p.t0;
       const int m = p.g * a.rpg + (TWO ? g * 128 : 0) + lr;    // this thread's row
@@ -400,30 +480,46 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           ds_fence_proxy_async_smem();
         }
         if (live) {
-          const bool masked = key0 + TA_KT > ctx;              // drafted nodes, or the end, among the keys
-          uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-          if (masked) {
+          // The loops stay loops: the body of a tile then fits the instruction caches. Masks are looked up
+          // where they are used, and only in tiles that hold nodes or the end of the keys.
+          const bool masked = key0 + TA_KT > ctx;
+          const int64_t nd = key0 - ctx;
+          float mx = -INFINITY, mg = 0.0f;
+          {
+            float va[32], vb[32];
+            auto look = [&](float (&v)[32], int c) {
+              if (CAP) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) bits[w] = ta_mask32(a, p.r, i, n, key0 + 32 * w - ctx);
-          }
-          float mx = -INFINITY;
+                for (int e = 0; e < 32; e += 2) mg = fmaxf(mg, fmaxf(fabsf(v[e]), fabsf(v[e + 1])));
+              }
+              if (masked) {
+                const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 32 * c);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            ds_tmem_ld_32x32b_x32(tS + 32 * c, v);
-            if (masked) {
+                for (int e = 0; e < 32; ++e) v[e] = (bits >> e) & 1u ? v[e] : -INFINITY;
+                __syncwarp();
+              }
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = (bits[c] >> e) & 1u ? v[e] : -INFINITY;
+              for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(v[e], v[e + 1]));
+            };
+            ta_tmem_fetch(tS, va);
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {
+              ta_arrived(va);
+              ta_tmem_fetch(tS + 32 * c + 32, vb);
+              look(va, c);
+              ta_arrived(vb);
+              if (c == 0) ta_tmem_fetch(tS + 64, va);
+              look(vb, c + 1);
             }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(v[e], v[e + 1]));
           }
+          float ya[16], yb[16];
+          ta_tmem_fetch(tS, ya);
           const float m2 = mx == -INFINITY ? -INFINITY : CAP ? ta_tanh(mx * sc, cap2) : mx * sc;
           const bool up = m2 > mref + TA_RISE || (mref == -INFINITY && m2 > -INFINITY);
           if (__any_sync(0xFFFFFFFFu, up)) {
             const float f = up ? ta_ex2(mref - m2) : 1.0f;     // 0 from -inf
             if (has) {
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < DP / 16; ++c) {
                 float o[16];
                 uint32_t w[16];
@@ -437,36 +533,54 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
             if (up) mref = m2;
           }
           const float mu = mref == -INFINITY ? 0.0f : mref;
-          const uint64_t sc2 = ds_f2(sc, sc), nm2 = ds_f2(-mu, -mu);
-          uint64_t sum = ds_f2(0.0f, 0.0f);
+          const uint64_t nm2 = ds_f2(-mu, -mu);
+          // the polynomial where every score of the warp is below the cap, else the exponential form
+          const bool poly = CAP && __all_sync(0xFFFFFFFFu, mg * sy <= 1.0f);
+          auto weigh = [&](float (&v)[16], int c) {
+            if (!CAP) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            uint32_t w[16];
-            ds_tmem_ld_32x32b_x32(tS + 32 * c, v);
+              for (int e = 0; e < 16; e += 2) {
+                const uint64_t x = ds_fma2(ds_f2(v[e], v[e + 1]), ds_f2(sc, sc), nm2);
+                v[e] = ds_f2lo(x);
+                v[e + 1] = ds_f2hi(x);
+              }
+            } else if (poly) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x0, x1;
-              if (CAP) {
-                x0 = ta_tanh(v[e] * sc, cap2) - mu;
-                x1 = ta_tanh(v[e + 1] * sc, cap2) - mu;
-              } else {
-                const uint64_t x = ds_fma2(ds_f2(v[e], v[e + 1]), sc2, nm2);
-                x0 = ds_f2lo(x);
-                x1 = ds_f2hi(x);
+              for (int e = 0; e < 16; e += 2) {
+                const uint64_t x = ds_fma2(ds_f2(v[e], v[e + 1]), tanh_poly.at(ds_f2(v[e], v[e + 1])), nm2);
+                v[e] = ds_f2lo(x);
+                v[e + 1] = ds_f2hi(x);
               }
-              if (masked) {
-                x0 = (bits[c] >> e) & 1u ? x0 : -INFINITY;
-                x1 = (bits[c] >> (e + 1)) & 1u ? x1 : -INFINITY;
-              }
-              x0 = ta_ex2(x0);
-              x1 = ta_ex2(x1);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = ta_tanh(v[e] * sc, cap2) - mu;
+            }
+            if (masked) {
+              const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 16 * c);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = (bits >> e) & 1u ? v[e] : -INFINITY;
+              __syncwarp();
+            }
+            uint32_t w[8];
+            uint64_t sum = ds_f2(0.0f, 0.0f);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float x0 = ta_ex2(v[e]), x1 = ta_ex2(v[e + 1]);
               sum = ds_add2(sum, ds_f2(x0, x1));
               w[e >> 1] = ta_pack(x0, x1);
             }
-            ta_tmem_st_x16(tS + 16 * c, w);
+            ta_tmem_st_x8(tS + 8 * c, w);
+            l += ds_f2lo(sum) + ds_f2hi(sum);
+          };
+#pragma unroll 1
+          for (int c = 0; c < 8; c += 2) {
+            ta_arrived(ya);
+            ta_tmem_fetch(tS + 16 * c + 16, yb);
+            weigh(ya, c);
+            ta_arrived(yb);
+            if (c < 6) ta_tmem_fetch(tS + 16 * c + 32, ya);
+            weigh(yb, c + 1);
           }
-          l += ds_f2lo(sum) + ds_f2hi(sum);
           ta_tmem_wait_st();
         }
         has = true;
@@ -503,9 +617,9 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
         const int h = p.hk * a.G + m - i * a.G;
         const int64_t row = int64_t(p.r) * a.T + i;
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + row * a.ldo + int64_t(h) * D;
-        float4* part = a.part_o + slot * (D / 4) * a.rs + (m - p.g * a.rpg);
+        float* part = a.part_o + (slot * a.rs + (m - p.g * a.rpg)) * D;
         float chk = 0.0f;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < (TWO ? DP : DP / 2) / 16; ++c) {
           const int d = d0 + 16 * c;
           float o[16];
@@ -539,7 +653,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
             } else {
 #pragma unroll
               for (int e = 0; e < 16; e += 4)
-                if (d + e < D) part[int64_t((d + e) >> 2) * a.rs] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                if (d + e < D) *reinterpret_cast<float4*>(part + d + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
         }
@@ -556,11 +670,11 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           const int mm = __shfl_sync(0xFFFFFFFFu, m, src);
           const float mr = __shfl_sync(0xFFFFFFFFu, mref, src), iv = __shfl_sync(0xFFFFFFFFu, inv, src);
           const int ii = mm / a.G;
-          ta_row_again(a, p.r, p.hk, mm, int64_t(p.t0) * TA_KT, int64_t(p.t1) * TA_KT, mr, iv, d0, min(d1, D),
+          ta_row_again(a, p.r, ctx, n, p.hk, mm, int64_t(p.t0) * TA_KT, int64_t(p.t1) * TA_KT, mr, iv, d0, min(d1, D),
                        whole ? reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t(p.r) * a.T + ii) * a.ldo +
                                    int64_t(p.hk * a.G + mm - ii * a.G) * D
                              : nullptr,
-                       a.part_o + slot * (D / 4) * a.rs + (mm - p.g * a.rpg));
+                       a.part_o + (slot * a.rs + (mm - p.g * a.rpg)) * D);
         }
       }
       ds_tc_fence_before();
@@ -577,59 +691,95 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
   }
 }
 
-// Joins the partial results of one item's rows: thread (row, four columns), the parts in the order of
-// the blocks that left them. Blocks whose item was finished by one block alone leave at once.
+// Joins the partial results of one row, one warp: the lanes take the parts' maxima and sums (a lane the
+// parts lane, lane + 32, ..), then the columns, adding the parts in the order of the blocks that left
+// them. Rows whose item was finished by one block are left at once.
 template <typename T>
-__global__ void __launch_bounds__(256) tree_attn_join_kernel(const TaArgs a, int32_t grid, int32_t nrb) {
+__global__ void __launch_bounds__(256) tree_attn_join_kernel(const TaArgs a, int32_t grid, int64_t jobs) {
   ds_pdl_trigger();
   ds_pdl_wait();
-  const int64_t item = blockIdx.x / nrb;
-  const int rb = int(blockIdx.x - item * nrb);
-  const int64_t hm = int64_t(a.c.heads) * a.mg;
-  const int r = int(item / hm);
-  const int64_t sub = item - r * hm;
-  const int hk = int(sub / a.mg), g = int(sub - int64_t(hk) * a.mg);
-  const int64_t total = int64_t(a.pref[a.R]) * hm, nt = a.pref[r + 1] - a.pref[r], g0 = int64_t(a.pref[r]) * hm + sub * nt;
-  const int64_t b0 = ((g0 + 1) * grid + total - 1) / total - 1;          // block that holds tile g0
-  if (total * (b0 + 1) / grid >= g0 + nt) return;                       // whole
-  const int64_t b1 = ((g0 + nt) * grid + total - 1) / total - 1;        // block of the last tile
-  const int D = a.c.head_dim;
-  const int lrow = rb * 8 + (threadIdx.x & 7), m = g * a.rpg + lrow;
-  if (lrow >= a.rpg || m >= a.rows) return;
-  float M = -INFINITY;
-  for (int64_t b = b0; b <= b1; ++b) {
-    if (total * (b + 1) / grid == total * b / grid) continue;
-    M = fmaxf(M, a.part_ml[(2 * b + (total * b / grid > g0 ? 0 : 1)) * a.rs + lrow].x);
-  }
-  const int i = m / a.G, h = hk * a.G + m - i * a.G;
+  const int64_t job = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (job >= jobs) return;
+  const int64_t item = ta_div(job, uint32_t(a.rs));
+  const int lrow = int(job - item * a.rs);
+  const int hm = a.c.heads * a.mg;
+  const int r = int(ta_div(item, uint32_t(hm))), sub = int(item - int64_t(r) * hm);
+  const int hk = sub / a.mg, g = sub - hk * a.mg, m = g * a.rpg + lrow;
+  const int64_t total = int64_t(a.pref[a.R]) * hm, p0 = a.pref[r], nt = a.pref[r + 1] - p0, g0 = p0 * hm + sub * nt;
+  const uint32_t ut = total > 0xFFFFFFFFll ? 0u : uint32_t(total);
+  auto holder = [&](int64_t tile) {                    // block whose share holds the tile
+    const int64_t x = (tile + 1) * grid + total - 1;
+    return int((ut ? ta_div(x, ut) : x / total) - 1);
+  };
+  const int b0 = holder(g0);
+  if (m >= a.rows || a.start[b0 + 1] >= g0 + nt) return;                // whole
+  const int np = holder(g0 + nt - 1) - b0 + 1;
+  const int i = m / a.G, h = hk * a.G + m - i * a.G, D = a.c.head_dim;
   const int64_t row = int64_t(r) * a.T + i;
-  for (int c = threadIdx.x >> 3; c < D / 4; c += 32) {
-    float L = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int64_t b = b0; b <= b1; ++b) {
-      if (total * (b + 1) / grid == total * b / grid) continue;
-      const int64_t slot = 2 * b + (total * b / grid > g0 ? 0 : 1);
+  auto part = [&](int k, int64_t& slot) {              // part k: block b0 + k, if its share is not empty
+    const int64_t s0 = a.start[b0 + k];
+    slot = 2 * int64_t(b0 + k) + (s0 > g0 ? 0 : 1);
+    return a.start[b0 + k + 1] > s0;
+  };
+  float M = -INFINITY;
+  for (int k = lane; k < np; k += 32) {
+    int64_t slot;
+    if (part(k, slot)) M = fmaxf(M, a.part_ml[slot * a.rs + lrow].x);
+  }
+  M = ds_warp_max(M);
+  float L = 0.0f;
+  float4 o[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  for (int k0 = 0; k0 < np; k0 += 32) {
+    const int k = k0 + lane;
+    int64_t slot = -1;
+    float w = 0.0f;
+    if (k < np && part(k, slot)) {
       const float2 ml = a.part_ml[slot * a.rs + lrow];
-      if (ml.y == 0.0f) continue;                      // nothing seen (a sum that is not a number goes on)
-      const float w = ta_ex2(ml.x - M);
-      const float4 x = a.part_o[(slot * (D / 4) + c) * a.rs + lrow];
-      L = __fmaf_rn(w, ml.y, L);
-      o.x = __fmaf_rn(w, x.x, o.x);
-      o.y = __fmaf_rn(w, x.y, o.y);
-      o.z = __fmaf_rn(w, x.z, o.z);
-      o.w = __fmaf_rn(w, x.w, o.w);
+      if (ml.y != 0.0f) {                              // something seen (also a sum that is not a number)
+        w = ta_ex2(ml.x - M);
+        L = __fmaf_rn(w, ml.y, L);
+      } else {
+        slot = -1;
+      }
+    } else {
+      slot = -1;
     }
-    const bool any = L != 0.0f;
-    const float inv = any ? 1.0f / L : 0.0f;
-    T* out = reinterpret_cast<T*>(a.out) + row * a.ldo + int64_t(h) * D + 4 * c;
-    const float y[4] = {any ? o.x * inv : 0.0f, any ? o.y * inv : 0.0f, any ? o.z * inv : 0.0f, any ? o.w * inv : 0.0f};
+    const int cnt = min(32, np - k0);
+#pragma unroll 4
+    for (int e = 0; e < cnt; ++e) {
+      const int64_t se = __shfl_sync(0xFFFFFFFFu, slot, e);
+      const float we = __shfl_sync(0xFFFFFFFFu, w, e);
+      if (se < 0) continue;
+      const float* x = a.part_o + (se * a.rs + lrow) * D;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int d = lane * 4 + 128 * u;
+        if (d >= D) continue;
+        const float4 y = *reinterpret_cast<const float4*>(x + d);
+        o[u].x = __fmaf_rn(we, y.x, o[u].x);
+        o[u].y = __fmaf_rn(we, y.y, o[u].y);
+        o[u].z = __fmaf_rn(we, y.z, o[u].z);
+        o[u].w = __fmaf_rn(we, y.w, o[u].w);
+      }
+    }
+  }
+  L = ds_warp_sumf(L);
+  const bool any = L != 0.0f;
+  const float inv = any ? 1.0f / L : 0.0f;
+  T* out = reinterpret_cast<T*>(a.out) + row * a.ldo + int64_t(h) * D;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int d = lane * 4 + 128 * u;
+    if (d >= D) continue;
+    const float y[4] = {any ? o[u].x * inv : 0.0f, any ? o[u].y * inv : 0.0f, any ? o[u].z * inv : 0.0f, any ? o[u].w * inv : 0.0f};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if constexpr (sizeof(T) == 2) out[e] = __float2bfloat16_rn(y[e]);
-      else out[e] = y[e];
+      if constexpr (sizeof(T) == 2) out[d + e] = __float2bfloat16_rn(y[e]);
+      else out[d + e] = y[e];
     }
-    if (c == 0 && a.lse) a.lse[row * a.Hq + h] = any ? (M + log2f(L)) * TA_LN2 : -INFINITY;
   }
+  if (lane == 0 && a.lse) a.lse[row * a.Hq + h] = any ? (M + log2f(L)) * TA_LN2 : -INFINITY;
 }
 
 // Tensor map of one buffer of the cache: (column, place, head, page), boxes of 64 columns x `box` places.
@@ -659,6 +809,7 @@ cudaError_t ta_dispatch_tc(const TaArgs& a, int grid, const CUtensorMap& k, cons
 }
 
 constexpr size_t TA_WS_PREF = 4352;        // pref[TA_MAXR + 1], rounded up to 256 bytes
+inline size_t ta_ws_head(int64_t grid) { return TA_WS_PREF + size_t(ds_ceil_div((grid + 1) * 8, 256) * 256); }
 
 }  // namespace
 
@@ -669,7 +820,7 @@ extern "C" size_t dspark_internal_ws_tree_attention(int64_t R, int32_t T, int64_
   if (R <= 0 || T <= 0 || cols <= 0 || heads <= 0) return 0;
   const int64_t vals = std::min<int64_t>(int64_t(T) * (cols / heads), 256 * 256);
   const int64_t slots = 2 * int64_t(ds_num_sms());
-  return TA_WS_PREF + size_t(ds_ceil_div(slots * vals * 5, 256) * 256);
+  return ta_ws_head(slots / 2) + size_t(ds_ceil_div(slots * vals * 5, 256) * 256);
 }
 
 extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64_t R, int32_t T, int32_t Hq,
@@ -704,20 +855,20 @@ extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64
   a.rpg = maps ? (a.rows > 128 ? 256 : 128) : 64;
   a.mg = int32_t(ds_ceil_div(a.rows, a.rpg));
   a.rs = std::min(a.rows, a.rpg);
-  const int nrb = int(ds_ceil_div(a.rs, 8));
-  const int64_t jobs = R * cache->heads * int64_t(a.mg) * nrb;
+  const int64_t jobs = R * cache->heads * int64_t(a.mg) * a.rs;         // rows of all items
   DS_REQUIRE(jobs <= INT32_MAX);
   const int grid = ds_num_sms();
   const int64_t slots = 2 * int64_t(grid);
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   a.pref = reinterpret_cast<int32_t*>(w);
-  a.part_o = reinterpret_cast<float4*>(w + TA_WS_PREF);
-  a.part_ml = reinterpret_cast<float2*>(w + TA_WS_PREF + size_t(slots) * a.rs * D * 4);
+  a.start = reinterpret_cast<int64_t*>(w + TA_WS_PREF);
+  a.part_o = reinterpret_cast<float*>(w + ta_ws_head(grid));
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * a.rs * D);
   if (maps) DS_CUDA_TRY(D <= 64 ? ta_dispatch_tc<64>(a, grid, mk, mv, stream) : ta_dispatch_tc<128>(a, grid, mk, mv, stream));
   else DS_CUDA_TRY(ta_launch_float(a, grid, stream));
   if (cache->dtype == DSPARK_BF16)
-    DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<__nv_bfloat16>, dim3(unsigned(jobs)), dim3(256), 0, stream, a, grid, nrb));
+    DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<__nv_bfloat16>, dim3(unsigned(ds_ceil_div(jobs, 8))), dim3(256), 0, stream, a, grid, jobs));
   else
-    DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<float>, dim3(unsigned(jobs)), dim3(256), 0, stream, a, grid, nrb));
+    DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<float>, dim3(unsigned(ds_ceil_div(jobs, 8))), dim3(256), 0, stream, a, grid, jobs));
   return DSPARK_OK;
 }

@@ -25,8 +25,9 @@ struct TaArgs {
   int32_t box;                 // keys per copy (tensor-core kernel)
   float scale, softcap;
   int32_t* pref;               // [R + 1] running sum of the requests' tile counts
+  int64_t* start;              // [blocks + 1] first tile of every block's share
   float2* part_ml;             // [slots][rs] (reference maximum in log2 units, sum)
-  float4* part_o;              // [slots][D / 4][rs] sums of weights times values, relative to the maximum
+  float* part_o;               // [slots][rs][D] sums of weights times values, relative to the maximum
   int32_t* status;
   uint32_t first_wait;
 };
@@ -45,83 +46,93 @@ struct TaPiece {
   DS_DEV int64_t slot(int64_t b) const { return 2 * b + (t0 > 0 ? 0 : 1); }
 };
 
+// The requests' running tile counts, committed lengths and node counts, in shared memory.
+struct TaLens {
+  int32_t pref[TA_MAXR + 1], ctx[TA_MAXR], n[TA_MAXR];
+};
+
+// Quotient of a number that rarely needs more than 32 bits.
+DS_DEV int64_t ta_div(int64_t x, uint32_t d) {
+  return (x >> 32) == 0 ? int64_t(uint32_t(x) / d) : x / int64_t(d);
+}
+
 struct TaWalk {
   int64_t at, end;
   int32_t r;
-  DS_DEV void init(const int32_t* pref, const TaArgs& a, int64_t b, int64_t grid) {
-    const int64_t hm = int64_t(a.c.heads) * a.mg, total = int64_t(pref[a.R]) * hm;
-    at = total * b / grid;
-    end = total * (b + 1) / grid;
+  DS_DEV void init(const TaLens& s, const TaArgs& a, int64_t b, uint32_t grid) {
+    const int64_t hm = int64_t(a.c.heads) * a.mg, total = s.pref[a.R] * hm;
+    at = ta_div(total * b, grid);
+    end = ta_div(total * (b + 1), grid);
     int lo = 0, hi = a.R;      // the last request that begins at or before `at`
     while (lo + 1 < hi) {
       const int mid = (lo + hi) >> 1;
-      if (int64_t(pref[mid]) * hm <= at) lo = mid;
+      if (s.pref[mid] * hm <= at) lo = mid;
       else hi = mid;
     }
     r = lo;
   }
-  DS_DEV bool next(const int32_t* pref, const TaArgs& a, TaPiece& p) {
+  DS_DEV bool next(const TaLens& s, const TaArgs& a, TaPiece& p) {
     if (at >= end) return false;
     const int64_t hm = int64_t(a.c.heads) * a.mg;
-    while (int64_t(pref[r + 1]) * hm <= at) ++r;
-    const int64_t off = at - int64_t(pref[r]) * hm;
+    while (s.pref[r + 1] * hm <= at) ++r;
+    const int64_t off = at - s.pref[r] * hm;
     p.r = r;
-    p.nt = pref[r + 1] - pref[r];
-    const int32_t item = int32_t(off / p.nt);
+    p.nt = s.pref[r + 1] - s.pref[r];
+    const int32_t item = int32_t(ta_div(off, uint32_t(p.nt)));
     p.t0 = int32_t(off - int64_t(item) * p.nt);
     p.t1 = int32_t(min(int64_t(p.nt), p.t0 + (end - at)));
-    p.hk = item / a.mg;
+    p.hk = int32_t(uint32_t(item) / uint32_t(a.mg));
     p.g = item - p.hk * a.mg;
     at += p.t1 - p.t0;
     return true;
   }
 };
 
-// Committed length and node count of request r; what is out of range is reported and cut so that no
-// slot past the page table is read.
-DS_DEV void ta_lens(const TaArgs& a, int r, int32_t& ctx, int32_t& n) {
-  ctx = a.ctx_len[r];
-  n = a.n_nodes ? a.n_nodes[r] : a.T;
-  if (n < 0 || n > a.T || ctx < 0) {
-    ds_set_error(a.status, DSPARK_EINVAL);
-    n = 0;
-    ctx = max(ctx, 0);
-  }
+// Lengths and running tile counts by all threads of the block. A length or node count out of range is
+// reported and cut so that no slot past the page table is read. Block 0 leaves the counts and every
+// block's first tile for the join.
+DS_DEV void ta_prefix(const TaArgs& a, TaLens& s) {
+  const int tid = threadIdx.x;
   const int64_t cap = int64_t(a.c.table_pages) * a.c.page_size;
-  if (int64_t(ctx) + n > cap) {
-    ds_set_error(a.status, DSPARK_ERANGE);
-    ctx = int32_t(min(int64_t(ctx), cap));
-    n = int32_t(min(int64_t(n), cap - ctx));
+  for (int r = tid; r < a.R; r += blockDim.x) {
+    int32_t ctx = a.ctx_len[r], n = a.n_nodes ? a.n_nodes[r] : a.T;
+    if (n < 0 || n > a.T || ctx < 0) {
+      ds_set_error(a.status, DSPARK_EINVAL);
+      n = 0;
+      ctx = max(ctx, 0);
+    }
+    if (int64_t(ctx) + n > cap) {
+      ds_set_error(a.status, DSPARK_ERANGE);
+      ctx = int32_t(min(int64_t(ctx), cap));
+      n = int32_t(min(int64_t(n), cap - ctx));
+    }
+    s.ctx[r] = ctx;
+    s.n[r] = n;
+    s.pref[r + 1] = max(1, int32_t((int64_t(ctx) + n + a.kt - 1) / a.kt));
   }
-}
-
-// pref[0..R] in shared memory, by all threads of the block.
-DS_DEV void ta_prefix(const TaArgs& a, int32_t* pref) {
-  for (int r = threadIdx.x; r < a.R; r += blockDim.x) {
-    int32_t ctx, n;
-    ta_lens(a, r, ctx, n);
-    pref[r + 1] = max(1, int32_t((int64_t(ctx) + n + a.kt - 1) / a.kt));
-  }
-  if (threadIdx.x == 0) pref[0] = 0;
+  if (tid == 0) s.pref[0] = 0;
   __syncthreads();
-  if (threadIdx.x < 32) {
+  if (tid < 32) {
     int32_t run = 0;
     for (int r0 = 0; r0 < a.R; r0 += 32) {
-      const int r = r0 + int(threadIdx.x);
-      int32_t v = r < a.R ? pref[r + 1] : 0;
+      const int r = r0 + tid;
+      int32_t v = r < a.R ? s.pref[r + 1] : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int32_t up = __shfl_up_sync(0xFFFFFFFFu, v, d);
-        if (int(threadIdx.x) >= d) v += up;
+        if (tid >= d) v += up;
       }
       v += run;
-      if (r < a.R) pref[r + 1] = v;
+      if (r < a.R) s.pref[r + 1] = v;
       run = __shfl_sync(0xFFFFFFFFu, v, 31);
     }
   }
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int r = threadIdx.x; r <= a.R; r += blockDim.x) a.pref[r] = pref[r];
+  if (blockIdx.x == 0) {
+    for (int r = tid; r <= a.R; r += blockDim.x) a.pref[r] = s.pref[r];
+    const int64_t total = s.pref[a.R] * (int64_t(a.c.heads) * a.mg);
+    for (int b = tid; b <= int(gridDim.x); b += blockDim.x) a.start[b] = ta_div(total * b, gridDim.x);
+  }
 }
 
 // Bits of the 32 keys whose first is node `nd` (negative: committed slots, which every node sees),
@@ -162,8 +173,8 @@ DS_DEV float ta_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// cap * tanh(x) with tanh(x) = 1 - 2 / (1 + e^(2 x)); `x2` is 2 x log2(e). Its error, about 2^-22 of the
-// cap whatever x, is far below what a tanh instruction leaves (about 2^-11).
+// cap * tanh(x) with tanh(x) = 1 - 2 / (1 + e^(2 x)); `x2` is 2 x log2(e). Its error is about 2^-22 of
+// the cap whatever x (a tanh instruction leaves about 2^-11).
 DS_DEV float ta_tanh(float x2, float cap) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ta_ex2(x2)));

@@ -47,7 +47,7 @@ DS_DEV float tf_rowsum(float x) {
 template <typename T, int U>
 __global__ void __launch_bounds__(TF_THREADS) tree_attn_float_kernel(const TaArgs a, bool vecq, bool veckv) {
   extern __shared__ float4 smem4[];
-  __shared__ int32_t s_pref[TA_MAXR + 1];
+  __shared__ TaLens s_len;
   __shared__ int64_t s_at[TF_KEYS];
   const int D = a.c.head_dim, ld = D + 4, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   float* sQ = reinterpret_cast<float*>(smem4);
@@ -56,14 +56,13 @@ __global__ void __launch_bounds__(TF_THREADS) tree_attn_float_kernel(const TaArg
   float* sP = sV + TF_KEYS * D;
   ds_pdl_trigger();
   ds_pdl_wait();
-  ta_prefix(a, s_pref);
+  ta_prefix(a, s_len);
   TaWalk walk;
-  walk.init(s_pref, a, blockIdx.x, gridDim.x);
+  walk.init(s_len, a, blockIdx.x, gridDim.x);
   TaPiece p;
   const T* q = reinterpret_cast<const T*>(a.q);
-  while (walk.next(s_pref, a, p)) {
-    int32_t ctx, n;
-    ta_lens(a, p.r, ctx, n);
+  while (walk.next(s_len, a, p)) {
+    const int32_t ctx = s_len.ctx[p.r], n = s_len.n[p.r];
     const int64_t len = int64_t(ctx) + n;
     const T* kc = reinterpret_cast<const T*>(a.c.k) + p.hk * a.c.head_stride;
     const T* vc = reinterpret_cast<const T*>(a.c.v) + p.hk * a.c.head_stride;
@@ -199,7 +198,8 @@ __global__ void __launch_bounds__(TF_THREADS) tree_attn_float_kernel(const TaArg
         const int d = tx * 4 + 64 * u;
         if (d >= D) break;
         if (!whole) {
-          a.part_o[(slot * (D / 4) + (d >> 2)) * a.rs + lr] = make_float4(o[x][4 * u], o[x][4 * u + 1], o[x][4 * u + 2], o[x][4 * u + 3]);
+          *reinterpret_cast<float4*>(a.part_o + (slot * a.rs + lr) * D + d) =
+              make_float4(o[x][4 * u], o[x][4 * u + 1], o[x][4 * u + 2], o[x][4 * u + 3]);
         } else {
           T* out = reinterpret_cast<T*>(a.out) + row * a.ldo + int64_t(h) * D + d;
 #pragma unroll
