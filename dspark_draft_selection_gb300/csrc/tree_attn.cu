@@ -16,8 +16,8 @@
 // only when a row's maximum rises by more than 2^8 (the weights stay below 256; sums are relative to
 // the same reference, so the result is the same softmax).
 //
-// Roles: warp 0 copies key and value tiles with TMA, one box per page piece, into a ring of stages;
-// warp 1 issues the MMAs; warps 2-3 copy the query rows; warps 4-7 and 8-11 are the softmax groups.
+// Roles: warps 0 and 2 copy key and value tiles with TMA, one box per page piece, into a ring of stages;
+// warp 1 issues the MMAs; warp 3 copies the query rows; warps 4-7 and 8-11 are the softmax groups.
 // Bound: HBM (2 D bytes of keys and of values per cached token and key head) up to about 270 query
 // rows per key head, the tensor pipe above.
 #include "tree_attn.cuh"
@@ -28,7 +28,7 @@ namespace {
 
 constexpr int TA_KT = 128;                 // keys per tile
 constexpr int TA_THREADS = 384;
-constexpr int TA_QTHREADS = 64;
+constexpr int TA_QTHREADS = 32;
 constexpr uint32_t TA_CHUNK = 128 * 128;   // bytes of 128 rows x 64 bf16 columns
 constexpr float TA_RISE = 8.0f;            // log2 rise of the maximum that rescales O
 
@@ -41,34 +41,44 @@ __host__ __device__ constexpr size_t ta_smem() {
   return 1024 + size_t(DP / 64) * TA_CHUNK * ((TWO ? 2 : 1) + ta_stages<DP, TWO>());
 }
 
-// 4-D tiled TMA load (column, place in page, head, page); what lies outside the tensor reads as zero.
+// 4-D tiled TMA load (column, place in page, head, page), what lies outside the tensor reading as zero,
+// by one elected lane of a warp that stays together.
 DS_DEV void ta_tma_load(void* dst, const void* tmap, int32_t d, int32_t t, int32_t h, int32_t p, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(ds_smem_addr(dst)),
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(ds_smem_addr(dst)),
       "l"(tmap), "r"(d), "r"(t), "r"(h), "r"(p), "r"(ds_smem_addr(bar))
       : "memory");
 }
 
 // The MMA warp stays together, so that descriptors and addresses are uniform registers, and one elected
-// lane - the same one every time - issues: D[tmem] (+)= A[smem] * B[smem], kind::f16,
-DS_DEV void ta_umma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// lane - the same one every time - issues: D[tmem] (+)= A[smem] * B[smem], kind::f16. A descriptor's low word
+// holds the address (in 16 bytes: all of shared memory fits its 14 bits, so offsets are plain additions) and
+// the leading offset; its high word is a constant of the layout.
+template <uint32_t HI>
+DS_DEV void ta_umma_ss(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "elect.sync _|e, 0xFFFFFFFF;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "r"(HI)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem],
-DS_DEV void ta_umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+template <uint32_t HI>
+DS_DEV void ta_umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "elect.sync _|e, 0xFFFFFFFF;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(idesc), "r"(accumulate), "r"(HI)
       : "memory");
 }
 // and the arrival on an mbarrier once everything issued before is complete.
@@ -116,37 +126,44 @@ DS_DEV void ta_arrived(float (&v)[16]) {
                  "+f"(v[15])::"memory");
 }
 
-// cap2 * tanh(sy * s) = s * Q(s^2) for |sy * s| <= 1: tanh(y) = y P(y^2) with the seven coefficients of P
-// that make the largest relative error smallest (5e-8, fitted by reweighted least squares; 1.6e-7 as
-// evaluated in float32), scaled by the powers of sy and by cap2; two values at a time.
+// cap2 * tanh(sy * s) = s * Q(s^2): tanh(y) = y P(y^2) with the coefficients of P that make the largest
+// relative error smallest (fitted by reweighted least squares), scaled by the powers of sy and by cap2; two
+// values at a time. Seven coefficients serve |y| <= 1 and four |y| <= 0.375; as evaluated in float32 their
+// errors are 1.6e-7 and 1.5e-7.
 struct TaTanhPoly {
-  float c[7];
+  float c[7], d[4];
   DS_DEV TaTanhPoly(float sy, float cap2) {
     const float p[7] = {0x1.fffffep-1f, -0x1.55540ap-2f, 0x1.10e672p-3f, -0x1.b5eb8p-5f, 0x1.4c6e4ap-6f, -0x1.968b3ap-8f, 0x1.10e592p-10f};
+    const float q[4] = {0x1.fffffep-1f, -0x1.5551c6p-2f, 0x1.10110cp-3f, -0x1.8b7242p-5f};
     float f = sy * cap2;
 #pragma unroll
-    for (int k = 0; k < 7; ++k, f *= sy * sy) c[k] = p[k] * f;
+    for (int k = 0; k < 7; ++k, f *= sy * sy) {
+      c[k] = p[k] * f;
+      if (k < 4) d[k] = q[k] * f;
+    }
   }
-  DS_DEV uint64_t at(uint64_t s) const {
+  DS_DEV uint64_t wide(uint64_t s) const {
     const uint64_t u = ds_fma2(s, s, 0);
     uint64_t q = ds_f2(c[6], c[6]);
 #pragma unroll
     for (int k = 5; k >= 0; --k) q = ds_fma2(q, u, ds_f2(c[k], c[k]));
     return q;
   }
+  DS_DEV uint64_t narrow(uint64_t s) const {
+    const uint64_t u = ds_fma2(s, s, 0);
+    uint64_t q = ds_f2(d[3], d[3]);
+#pragma unroll
+    for (int k = 2; k >= 0; --k) q = ds_fma2(q, u, ds_f2(d[k], d[k]));
+    return q;
+  }
 };
 
-// Descriptor of an operand whose N index is contiguous (V: rows are keys, 64 columns of D to a
-// 128-byte row): 64-column blocks lie TA_CHUNK apart, groups of eight keys 1024 bytes apart.
-DS_DEV uint64_t ta_desc_nmajor(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= uint64_t((saddr & 0x3FFFFu) >> 4);
-  d |= uint64_t(TA_CHUNK >> 4) << 16;
-  d |= uint64_t(1024 >> 4) << 32;
-  d |= uint64_t(1) << 46;
-  d |= uint64_t(2) << 61;
-  return d;
-}
+// High word of both layouts: groups of eight rows (K-major: query or key rows; N-major: keys) 1024 bytes
+// apart, descriptor version 1, 128-byte swizzle. Low words: K-major needs no leading offset; an operand
+// whose N index is contiguous (V: 64 columns of D to a 128-byte row) has its 64-column blocks TA_CHUNK apart.
+constexpr uint32_t TA_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+DS_DEV uint32_t ta_desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+DS_DEV uint32_t ta_desc_n(uint32_t saddr) { return (saddr >> 4) | ((TA_CHUNK >> 4) << 16); }
 
 DS_DEV void ta_tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
@@ -218,7 +235,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
   constexpr uint32_t TS = 0, TO = 256;                 // tensor memory: S of group g at 128 g, O at 256 + DP g
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[NS], s_empty[NS], s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_ofull, s_ofree, s_mlfull, s_drain;
-  __shared__ uint32_t s_tmem;
+  __shared__ uint32_t s_tmem, s_seq[NS];               // s_seq: sequence number + 1 of a stage's last copy
   __shared__ int s_abort;
   __shared__ TaLens s_len;
   __shared__ float2 s_ml[2][2][128];                   // [piece parity][group][row]
@@ -228,10 +245,15 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
   uint8_t* sR = sQ + (TWO ? 2 : 1) * STAGE;            // the ring (a query tile has a stage's size)
 
   ds_pdl_trigger();
+  if (tid == 64) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tmK) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tmV) : "memory");
+  }
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       ds_mbar_init(&s_full[s], 1);
       ds_mbar_init(&s_empty[s], 1);
+      s_seq[s] = 0;
     }
     ds_mbar_init(&s_qfull, TA_QTHREADS);
     ds_mbar_init(&s_qempty, 1);
@@ -254,82 +276,79 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
   auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t limit) {
-    if (!ds_mbar_wait_or_abort(bar, parity & 1u, limit, &s_abort)) {
-      if (!aborted()) ds_set_error(a.status, DSPARK_ETIMEOUT);
-      s_abort = 1;
-    }
-    return !aborted();
+    if (ds_mbar_wait_or_abort(bar, parity & 1u, limit, &s_abort)) return true;
+    if (!aborted()) ds_set_error(a.status, DSPARK_ETIMEOUT);
+    s_abort = 1;
+    return false;
   };
   TaWalk walk;
-  walk.init(s_len, a, blockIdx.x, gridDim.x);
+  walk.init(s_len);
   TaPiece p;
 
-  if (warp == 0) {
-    // ---- key and value tiles: lane b copies box b (keys b * box ..) of a tile; the copy of a box past
-    // the last key, or of a page that does not exist, names a page past the last and reads zeros ----
+  if (warp == 0 || warp == 2) {
+    // ---- key tiles (warp 0) and value tiles (warp 2): lane b looks up the page of box b (keys b * box ..),
+    // then the boxes go out one after the other. The copy of a box past the last key, or of a page that
+    // does not exist, names a page past the last and reads zeros. The tiles lie in the ring in the order in
+    // which the MMA warp takes them: K0 V0 K1 V1 .. for two row tiles, else K0 K1 V0 K2 V1 K3 .. ----
+    const bool isv = warp == 2;
+    const CUtensorMap* tm = isv ? &tmV : &tmK;
     const int box = a.box, nbox = TA_KT / box;
-    uint32_t seq = 0;
+    uint32_t base = 0;                                 // sequence number of the piece's first tile
     bool ok = true;
     while (ok && walk.next(s_len, a, p)) {
-      const int32_t ctx = s_len.ctx[p.r], n = s_len.n[p.r];
-      const int64_t len = int64_t(ctx) + n;
+      const uint32_t len = uint32_t(s_len.ctx[p.r]) + uint32_t(s_len.n[p.r]), page = uint32_t(a.c.page_size);
       const int32_t* table = a.c.page_table + int64_t(p.r) * a.c.ld_table;
-      int32_t place = 0;
-      auto page_of = [&](int t) -> int64_t {           // (page, place) of this lane's box of tile t
-        int32_t pg = int32_t(a.c.num_pages);
-        const int64_t key = int64_t(t) * TA_KT + lane * box;
-        if (lane < nbox && t < p.t1 && key < len) {
-          const int64_t e = key / a.c.page_size;
-          place = int32_t(key - e * a.c.page_size);
+      const int npt = p.t1 - p.t0;
+      int32_t place = 0, pg = 0;
+      auto look_up = [&](int t) {                      // (page, place) of this lane's box of the piece's tile t
+        pg = int32_t(a.c.num_pages);
+        const uint32_t key = uint32_t(p.t0 + t) * TA_KT + uint32_t(lane * box);
+        if (lane < nbox && t < npt && key < len) {
+          const uint32_t e = key / page;
+          place = int32_t(key - e * page);
           pg = table[e];
           if (pg < 0 || pg >= a.c.num_pages) {
             ds_set_error(a.status, DSPARK_ERANGE);
             pg = int32_t(a.c.num_pages);
           }
         }
-        return (int64_t(place) << 32) | uint32_t(pg);
       };
-      auto load = [&](const CUtensorMap* tm, int64_t at) {
-        const uint32_t s = seq % NS, ph = (seq / NS) & 1u;
-        ok = wait(&s_empty[s], ph ^ 1u, DS_WAIT_LIMIT);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) return;
-        if (lane == 0) ds_mbar_arrive_expect_tx(&s_full[s], STAGE);
-        __syncwarp();
-        if (lane < nbox) {
-          uint8_t* dst = sR + s * STAGE + lane * box * 128;
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-            ta_tma_load(dst + c * TA_CHUNK, tm, c * 64, int32_t(at >> 32), p.hk, int32_t(at), &s_full[s]);
+      look_up(0);
+      for (int t = 0; t < npt; ++t) {
+        const uint32_t sq = base + (TWO ? 2 * t + (isv ? 1 : 0) : isv ? min(npt, t + 2) + t : t < 2 ? t : 2 * t - 1);
+        const uint32_t s = sq % NS;
+        const int32_t pg_t = pg, place_t = place;
+        look_up(t + 1);                                // on its way while this tile waits for its stage
+        ok = __all_sync(0xFFFFFFFFu, wait(&s_empty[s], (sq / NS + 1), DS_WAIT_LIMIT));
+        if (!ok) break;
+        if (lane == 0) {
+          s_seq[s] = sq + 1;
+          ds_mbar_arrive_expect_tx(&s_full[s], STAGE);
         }
         __syncwarp();
-        ++seq;
-      };
-      // the order in which the MMA warp consumes them
-      int64_t pa = page_of(p.t0), pb = page_of(p.t0 + 1);
-      load(&tmK, pa);
-      if (!TWO && ok && p.t0 + 1 < p.t1) load(&tmK, pb);
-      for (int t = p.t0; ok && t < p.t1; ++t) {
-        const int64_t pc = page_of(t + 2);
-        load(&tmV, pa);
-        if (ok && TWO && t + 1 < p.t1) load(&tmK, pb);
-        if (ok && !TWO && t + 2 < p.t1) load(&tmK, pc);
-        pa = pb;
-        pb = pc;
+#pragma unroll 1
+        for (int b = 0; b < nbox; ++b) {
+          const int32_t pb = __shfl_sync(0xFFFFFFFFu, pg_t, b), lb = __shfl_sync(0xFFFFFFFFu, place_t, b);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            ta_tma_load(sR + s * STAGE + c * TA_CHUNK + b * box * 128, tm, c * 64, lb, p.hk, pb, &s_full[s]);
+        }
       }
+      base += 2 * npt;
     }
-    if (lane == 0)                                     // every copy lands before the block leaves
-      for (uint32_t k = (seq > uint32_t(NS) ? seq - NS : 0); k < seq; ++k)
-        (void)ds_mbar_wait(&s_full[k % NS], (k / NS) & 1u, DS_WAIT_LIMIT);
+    // After a wait that ran out, the copies in flight land before the block leaves (otherwise the MMA warp
+    // has waited for every one of them).
+    for (int k = 0; k < NS && aborted(); ++k) {
+      const uint32_t v = *reinterpret_cast<volatile uint32_t*>(&s_seq[k]);
+      if (v) (void)ds_mbar_wait(&s_full[k], ((v - 1) / NS) & 1u, DS_WAIT_LIMIT);
+    }
     __syncwarp();
   } else if (warp == 1) {
     // ---- one lane issues the MMAs. QK of a group's next tile follows the group's PV: S and P share
     // tensor memory, and the MMAs of one thread run in order ----
     constexpr uint32_t idS = ds_idesc_bf16_f32(128, TA_KT);
     constexpr uint32_t idO = ds_idesc_bf16_f32(128, DP) | (1u << 16);   // B is N-major
-    // addresses stay below 2^18, so a descriptor's address field (in 16 bytes) takes plain additions
-    const uint64_t qdesc = ds_smem_desc_sw128(ds_smem_addr(sQ)), kdesc = ds_smem_desc_sw128(ds_smem_addr(sR)),
-                   vdesc = ta_desc_nmajor(ds_smem_addr(sR));
+    const uint32_t qdesc = ta_desc_k(ds_smem_addr(sQ)), kdesc = ta_desc_k(ds_smem_addr(sR)), vdesc = ta_desc_n(ds_smem_addr(sR));
     uint32_t seq = 0, np = 0, pn[2] = {0, 0};
     bool ok = true;
     auto full = [&](uint32_t sq) {
@@ -339,19 +358,23 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     };
     auto release = [&](uint32_t sq) { ta_commit(&s_empty[sq % NS]); };
     auto qk = [&](int g, uint32_t sq) {
-      const uint64_t q0 = qdesc + (((TWO ? g : 0) * STAGE) >> 4), k0 = kdesc + (((sq % NS) * STAGE) >> 4);
+      const uint32_t q0 = __shfl_sync(0xFFFFFFFFu, qdesc + (((TWO ? g : 0) * STAGE) >> 4), 0);
+      const uint32_t k0 = __shfl_sync(0xFFFFFFFFu, kdesc + (((sq % NS) * STAGE) >> 4), 0);
+      const uint32_t d0 = __shfl_sync(0xFFFFFFFFu, tmem + TS + 128 * g, 0);
 #pragma unroll
       for (int kb = 0; kb < DP / 16; ++kb) {
         const uint32_t off = ((kb >> 2) * TA_CHUNK + (kb & 3) * 32) >> 4;
-        ta_umma_ss(tmem + TS + 128 * g, q0 + off, k0 + off, idS, kb != 0);
+        ta_umma_ss<TA_DESC_HI>(d0, q0 + off, k0 + off, idS, kb != 0);
       }
       ta_commit(&s_sfull[g]);
     };
     auto pv = [&](int g, uint32_t sq, bool acc) {
-      const uint64_t v0 = vdesc + (((sq % NS) * STAGE) >> 4);
+      const uint32_t v0 = __shfl_sync(0xFFFFFFFFu, vdesc + (((sq % NS) * STAGE) >> 4), 0);
+      const uint32_t d0 = __shfl_sync(0xFFFFFFFFu, tmem + TO + DP * g, 0), a0 = __shfl_sync(0xFFFFFFFFu, tmem + TS + 128 * g, 0);
+      const uint32_t acc0 = __shfl_sync(0xFFFFFFFFu, uint32_t(acc), 0);
 #pragma unroll
       for (int kb = 0; kb < TA_KT / 16; ++kb)
-        ta_umma_ts(tmem + TO + DP * g, tmem + TS + 128 * g + kb * 8, v0 + ((kb * 2048) >> 4), idO, acc || kb != 0);
+        ta_umma_ts<TA_DESC_HI>(d0, a0 + kb * 8, v0 + ((kb * 2048) >> 4), idO, kb ? 1u : acc0);
     };
     auto weights = [&](int g, bool first) {          // P of group g is written; at first O must be free too
       ok = ok && wait(&s_pfull[g], pn[g]++, DS_WAIT_LIMIT);
@@ -417,7 +440,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     // ---- query rows of each piece into the swizzled layout; columns past head_dim are zero (the key
     // tile's are too), rows that do not exist keep what was there: a row only reaches its own results ----
     constexpr int CPR = DP / 8, STEP = TA_QTHREADS / CPR;        // 16-byte columns of a row, rows per round
-    const int qt = tid - 64, c = qt % CPR, D = a.c.head_dim;
+    const int qt = lane, c = qt % CPR, D = a.c.head_dim;
     uint32_t np = 0;
     const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + c * 8;
     uint8_t* dst = sQ + (c >> 3) * TA_CHUNK;
@@ -480,10 +503,26 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           ds_fence_proxy_async_smem();
         }
         if (live) {
-          // The loops stay loops: the body of a tile then fits the instruction caches. Masks are looked up
-          // where they are used, and only in tiles that hold nodes or the end of the keys.
+          // Masks matter only in tiles that hold nodes or the end of the keys. Without a cap they are put
+          // into S beforehand; with one they are looked up after it, and the longer code stays in loops (as
+          // straight lines it waits for instructions more than it saves).
+          constexpr int FLAT = CAP ? 1 : 8;
           const bool masked = key0 + TA_KT > ctx;
           const int64_t nd = key0 - ctx;
+          if (!CAP && masked) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              float v[16];
+              uint32_t w[16];
+              ds_tmem_ld_32x32b_x16(tS + 16 * c, v);
+              const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 16 * c);
+              __syncwarp();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = (bits >> e) & 1u ? __float_as_uint(v[e]) : 0xFF800000u;
+              ta_tmem_st_x16(tS + 16 * c, w);
+            }
+            ta_tmem_wait_st();
+          }
           float mx = -INFINITY, mg = 0.0f;
           {
             float va[32], vb[32];
@@ -492,7 +531,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) mg = fmaxf(mg, fmaxf(fabsf(v[e]), fabsf(v[e + 1])));
               }
-              if (masked) {
+              if (CAP && masked) {
                 const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 32 * c);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = (bits >> e) & 1u ? v[e] : -INFINITY;
@@ -502,7 +541,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
               for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(v[e], v[e + 1]));
             };
             ta_tmem_fetch(tS, va);
-#pragma unroll 1
+#pragma unroll FLAT
             for (int c = 0; c < 4; c += 2) {
               ta_arrived(va);
               ta_tmem_fetch(tS + 32 * c + 32, vb);
@@ -534,8 +573,9 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           }
           const float mu = mref == -INFINITY ? 0.0f : mref;
           const uint64_t nm2 = ds_f2(-mu, -mu);
-          // the polynomial where every score of the warp is below the cap, else the exponential form
-          const bool poly = CAP && __all_sync(0xFFFFFFFFu, mg * sy <= 1.0f);
+          // the polynomials where every score of the warp is well below the cap, else the exponential form
+          const bool narrow = CAP && __all_sync(0xFFFFFFFFu, mg * sy <= 0.375f);
+          const bool wide = CAP && __all_sync(0xFFFFFFFFu, mg * sy <= 1.0f);
           auto weigh = [&](float (&v)[16], int c) {
             if (!CAP) {
 #pragma unroll
@@ -544,10 +584,17 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
                 v[e] = ds_f2lo(x);
                 v[e + 1] = ds_f2hi(x);
               }
-            } else if (poly) {
+            } else if (narrow) {
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
-                const uint64_t x = ds_fma2(ds_f2(v[e], v[e + 1]), tanh_poly.at(ds_f2(v[e], v[e + 1])), nm2);
+                const uint64_t x = ds_fma2(ds_f2(v[e], v[e + 1]), tanh_poly.narrow(ds_f2(v[e], v[e + 1])), nm2);
+                v[e] = ds_f2lo(x);
+                v[e + 1] = ds_f2hi(x);
+              }
+            } else if (wide) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const uint64_t x = ds_fma2(ds_f2(v[e], v[e + 1]), tanh_poly.wide(ds_f2(v[e], v[e + 1])), nm2);
                 v[e] = ds_f2lo(x);
                 v[e + 1] = ds_f2hi(x);
               }
@@ -555,7 +602,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
 #pragma unroll
               for (int e = 0; e < 16; ++e) v[e] = ta_tanh(v[e] * sc, cap2) - mu;
             }
-            if (masked) {
+            if (CAP && masked) {
               const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 16 * c);
 #pragma unroll
               for (int e = 0; e < 16; ++e) v[e] = (bits >> e) & 1u ? v[e] : -INFINITY;
@@ -572,7 +619,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
             ta_tmem_st_x8(tS + 8 * c, w);
             l += ds_f2lo(sum) + ds_f2hi(sum);
           };
-#pragma unroll 1
+#pragma unroll FLAT
           for (int c = 0; c < 8; c += 2) {
             ta_arrived(ya);
             ta_tmem_fetch(tS + 16 * c + 16, yb);

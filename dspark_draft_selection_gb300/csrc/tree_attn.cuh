@@ -46,30 +46,27 @@ struct TaPiece {
   DS_DEV int64_t slot(int64_t b) const { return 2 * b + (t0 > 0 ? 0 : 1); }
 };
 
-// The requests' running tile counts, committed lengths and node counts, in shared memory.
+// The requests' running tile counts, committed lengths and node counts, and where the block's share
+// begins, in shared memory.
 struct TaLens {
   int32_t pref[TA_MAXR + 1], ctx[TA_MAXR], n[TA_MAXR];
+  int64_t at, end;
+  int32_t r;
 };
 
-// Quotient of a number that rarely needs more than 32 bits.
+// Quotient of a number that rarely needs more than 32 bits (the long division stays out of line).
+static __device__ __noinline__ int64_t ta_div64(int64_t x, int64_t d) { return x / d; }
 DS_DEV int64_t ta_div(int64_t x, uint32_t d) {
-  return (x >> 32) == 0 ? int64_t(uint32_t(x) / d) : x / int64_t(d);
+  return (x >> 32) == 0 ? int64_t(uint32_t(x) / d) : ta_div64(x, d);
 }
 
 struct TaWalk {
   int64_t at, end;
   int32_t r;
-  DS_DEV void init(const TaLens& s, const TaArgs& a, int64_t b, uint32_t grid) {
-    const int64_t hm = int64_t(a.c.heads) * a.mg, total = s.pref[a.R] * hm;
-    at = ta_div(total * b, grid);
-    end = ta_div(total * (b + 1), grid);
-    int lo = 0, hi = a.R;      // the last request that begins at or before `at`
-    while (lo + 1 < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s.pref[mid] * hm <= at) lo = mid;
-      else hi = mid;
-    }
-    r = lo;
+  DS_DEV void init(const TaLens& s) {
+    at = s.at;
+    end = s.end;
+    r = s.r;
   }
   DS_DEV bool next(const TaLens& s, const TaArgs& a, TaPiece& p) {
     if (at >= end) return false;
@@ -94,7 +91,7 @@ struct TaWalk {
 DS_DEV void ta_prefix(const TaArgs& a, TaLens& s) {
   const int tid = threadIdx.x;
   const int64_t cap = int64_t(a.c.table_pages) * a.c.page_size;
-  for (int r = tid; r < a.R; r += blockDim.x) {
+  auto take = [&](int r) -> int32_t {                  // request r's lengths; its tile count
     int32_t ctx = a.ctx_len[r], n = a.n_nodes ? a.n_nodes[r] : a.T;
     if (n < 0 || n > a.T || ctx < 0) {
       ds_set_error(a.status, DSPARK_EINVAL);
@@ -108,15 +105,18 @@ DS_DEV void ta_prefix(const TaArgs& a, TaLens& s) {
     }
     s.ctx[r] = ctx;
     s.n[r] = n;
-    s.pref[r + 1] = max(1, int32_t((int64_t(ctx) + n + a.kt - 1) / a.kt));
+    return max(1, int32_t(uint32_t(uint32_t(ctx) + uint32_t(n) + uint32_t(a.kt - 1)) / uint32_t(a.kt)));
+  };
+  const bool few = a.R <= 64;                          // one warp is enough, with one synchronisation less
+  if (!few) {
+    for (int r = tid; r < a.R; r += blockDim.x) s.pref[r + 1] = take(r);
+    __syncthreads();
   }
-  if (tid == 0) s.pref[0] = 0;
-  __syncthreads();
   if (tid < 32) {
     int32_t run = 0;
     for (int r0 = 0; r0 < a.R; r0 += 32) {
       const int r = r0 + tid;
-      int32_t v = r < a.R ? s.pref[r + 1] : 0;
+      int32_t v = r >= a.R ? 0 : few ? take(r) : s.pref[r + 1];
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int32_t up = __shfl_up_sync(0xFFFFFFFFu, v, d);
@@ -125,6 +125,21 @@ DS_DEV void ta_prefix(const TaArgs& a, TaLens& s) {
       v += run;
       if (r < a.R) s.pref[r + 1] = v;
       run = __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    if (tid == 0) s.pref[0] = 0;
+    __syncwarp();
+    // the block's share and the last request that begins at or before it
+    const int64_t hm = int64_t(a.c.heads) * a.mg, total = run * hm, at = ta_div(total * blockIdx.x, gridDim.x);
+    int r = 0;
+    for (int r0 = 0; r0 < a.R; r0 += 32) {
+      const unsigned before = __ballot_sync(0xFFFFFFFFu, r0 + tid < a.R && s.pref[min(r0 + tid, a.R - 1)] * hm <= at);
+      if (before) r = r0 + 31 - __clz(int(before));
+      if (before != 0xFFFFFFFFu) break;
+    }
+    if (tid == 0) {
+      s.at = at;
+      s.end = ta_div(total * (blockIdx.x + 1), gridDim.x);
+      s.r = r;
     }
   }
   __syncthreads();

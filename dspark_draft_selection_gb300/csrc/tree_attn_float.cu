@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(TF_THREADS) tree_attn_float_kernel(const TaArg
   ds_pdl_wait();
   ta_prefix(a, s_len);
   TaWalk walk;
-  walk.init(s_len, a, blockIdx.x, gridDim.x);
+  walk.init(s_len);
   TaPiece p;
   const T* q = reinterpret_cast<const T*>(a.q);
   while (walk.next(s_len, a, p)) {
