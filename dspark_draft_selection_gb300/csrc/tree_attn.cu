@@ -523,13 +523,14 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
             }
             ta_tmem_wait_st();
           }
-          float mx = -INFINITY, mg = 0.0f;
+          // chains of four maxima, and below of four sums, side by side: one would wait for itself
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mg4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           {
             float va[32], vb[32];
             auto look = [&](float (&v)[32], int c) {
               if (CAP) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) mg = fmaxf(mg, fmaxf(fabsf(v[e]), fabsf(v[e + 1])));
+                for (int e = 0; e < 32; e += 2) mg4[(e >> 1) & 3] = fmaxf(mg4[(e >> 1) & 3], fmaxf(fabsf(v[e]), fabsf(v[e + 1])));
               }
               if (CAP && masked) {
                 const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 32 * c);
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
                 __syncwarp();
               }
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(v[e], v[e + 1]));
+              for (int e = 0; e < 32; e += 2) mx4[(e >> 1) & 3] = fmaxf(mx4[(e >> 1) & 3], fmaxf(v[e], v[e + 1]));
             };
             ta_tmem_fetch(tS, va);
 #pragma unroll FLAT
@@ -551,8 +552,10 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
               look(vb, c + 1);
             }
           }
-          float ya[16], yb[16];
-          ta_tmem_fetch(tS, ya);
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          const float mg = fmaxf(fmaxf(mg4[0], mg4[1]), fmaxf(mg4[2], mg4[3]));
+          float v[16];
+          ta_tmem_fetch(tS, v);
           const float m2 = mx == -INFINITY ? -INFINITY : CAP ? ta_tanh(mx * sc, cap2) : mx * sc;
           const bool up = m2 > mref + TA_RISE || (mref == -INFINITY && m2 > -INFINITY);
           if (__any_sync(0xFFFFFFFFu, up)) {
@@ -576,58 +579,69 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           // the polynomials where every score of the warp is well below the cap, else the exponential form
           const bool narrow = CAP && __all_sync(0xFFFFFFFFu, mg * sy <= 0.375f);
           const bool wide = CAP && __all_sync(0xFFFFFFFFu, mg * sy <= 1.0f);
-          auto weigh = [&](float (&v)[16], int c) {
-            if (!CAP) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const uint64_t x = ds_fma2(ds_f2(v[e], v[e + 1]), ds_f2(sc, sc), nm2);
-                v[e] = ds_f2lo(x);
-                v[e + 1] = ds_f2hi(x);
-              }
-            } else if (narrow) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const uint64_t x = ds_fma2(ds_f2(v[e], v[e + 1]), tanh_poly.narrow(ds_f2(v[e], v[e + 1])), nm2);
-                v[e] = ds_f2lo(x);
-                v[e + 1] = ds_f2hi(x);
-              }
-            } else if (wide) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const uint64_t x = ds_fma2(ds_f2(v[e], v[e + 1]), tanh_poly.wide(ds_f2(v[e], v[e + 1])), nm2);
-                v[e] = ds_f2lo(x);
-                v[e + 1] = ds_f2hi(x);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = ta_tanh(v[e] * sc, cap2) - mu;
-            }
-            if (CAP && masked) {
-              const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 16 * c);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = (bits >> e) & 1u ? v[e] : -INFINITY;
-              __syncwarp();
-            }
+          uint64_t sum[4] = {0, 0, 0, 0};
+          auto put = [&](const uint64_t (&x)[8], int c) {      // weights of 16 keys: exponentials, sums, P
             uint32_t w[8];
-            uint64_t sum = ds_f2(0.0f, 0.0f);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const float x0 = ta_ex2(v[e]), x1 = ta_ex2(v[e + 1]);
-              sum = ds_add2(sum, ds_f2(x0, x1));
-              w[e >> 1] = ta_pack(x0, x1);
+            for (int e = 0; e < 8; ++e) {
+              const float x0 = ta_ex2(ds_f2lo(x[e])), x1 = ta_ex2(ds_f2hi(x[e]));
+              sum[e & 3] = ds_add2(sum[e & 3], ds_f2(x0, x1));
+              w[e] = ta_pack(x0, x1);
             }
             ta_tmem_st_x8(tS + 8 * c, w);
-            l += ds_f2lo(sum) + ds_f2hi(sum);
           };
-#pragma unroll FLAT
-          for (int c = 0; c < 8; c += 2) {
-            ta_arrived(ya);
-            ta_tmem_fetch(tS + 16 * c + 16, yb);
-            weigh(ya, c);
-            ta_arrived(yb);
-            if (c < 6) ta_tmem_fetch(tS + 16 * c + 32, ya);
-            weigh(yb, c + 1);
+          auto exponents = [&](uint64_t (&x)[8]) {             // the common forms, one pair of scores at a time
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint64_t y = ds_f2(v[2 * e], v[2 * e + 1]);
+              x[e] = ds_fma2(y, CAP ? tanh_poly.narrow(y) : ds_f2(sc, sc), nm2);
+            }
+          };
+          if (!CAP || (narrow && !masked)) {
+            // 16 keys' FMAs beside the 16 keys' exponentials before them: one warp alone keeps both pipes busy
+            uint64_t x[2][8];
+            ta_arrived(v);
+            exponents(x[0]);
+            ta_tmem_fetch(tS + 16, v);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              if (c < 7) {
+                ta_arrived(v);
+                exponents(x[(c + 1) & 1]);
+                if (c < 6) ta_tmem_fetch(tS + 16 * c + 32, v);
+              }
+              put(x[c & 1], c);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint64_t x[8];
+              ta_arrived(v);
+              if (narrow) {
+                exponents(x);
+              } else if (wide) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const uint64_t y = ds_f2(v[2 * e], v[2 * e + 1]);
+                  x[e] = ds_fma2(y, tanh_poly.wide(y), nm2);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = ds_f2(ta_tanh(v[2 * e] * sc, cap2) - mu, ta_tanh(v[2 * e + 1] * sc, cap2) - mu);
+              }
+              if (masked) {
+                const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 16 * c);
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  x[e] = ds_f2((bits >> (2 * e)) & 1u ? ds_f2lo(x[e]) : -INFINITY, (bits >> (2 * e + 1)) & 1u ? ds_f2hi(x[e]) : -INFINITY);
+              }
+              if (c < 7) ta_tmem_fetch(tS + 16 * c + 16, v);
+              put(x, c);
+            }
           }
+          sum[0] = ds_add2(ds_add2(sum[0], sum[1]), ds_add2(sum[2], sum[3]));
+          l += ds_f2lo(sum[0]) + ds_f2hi(sum[0]);
           ta_tmem_wait_st();
         }
         has = true;
