@@ -10,8 +10,8 @@
 
 namespace {
 
-constexpr int RA_THREADS = 256;
-constexpr int RA_MAXROWS = 4;
+constexpr int RA_THREADS = 128;
+constexpr int RA_MAXROWS = 2;
 constexpr int CM_THREADS = 128;
 constexpr int CM_MAXT = 512;
 constexpr int CM_BATCH = 8;
@@ -47,16 +47,20 @@ DS_DEV float ra_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 DS_DEV void ra_set(float& y, float x) { y = x; }
 DS_DEV void ra_set(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
 
-// Every byte moves once, so the kernel is bound by HBM for many rows and by latency for few. A block
-// takes NR node slots: their cosines and sines (gathered over the position axes) are staged in
-// shared memory once for all heads, then the threads go over the rows' work items, an item being VEC
-// columns of both halves of a rotated head (one load, one store each), VEC columns a head passes
-// through unrotated, or VEC columns of a value head. VEC * sizeof(T) is 16 bytes where the layout
-// allows, else one element. grid.y splits the items of a row when there are few rows.
+// Every byte moves once, so the kernel is bound by HBM for many rows and by latency for few. A block of 128
+// threads takes one or two node slots: their cosines and sines (gathered over the position axes) are staged in
+// shared memory once for all heads, then the threads go over the rows' work items, an item being VEC columns
+// of both halves of a rotated head, VEC columns a head passes through unrotated, or VEC columns of a value
+// head. VEC * sizeof(T) is 16 bytes where the layout allows, then four elements, else one. With few rows
+// grid.y splits the items of a row.
+// 12,002 rows of 32 + 2 x 8 heads of 128 bf16 columns, three axes: 46.9 us, 5.4 TB/s of the bytes that have to
+// move. What carries it is the number of blocks an SM holds (12, at 40 registers), since each waits for its
+// page and its table rows before it moves anything: blocks of 256 threads with four rows 49-51 us, items two
+// and three at a time (fewer blocks) 55 and 66 us, eight rows a block 58-64 us.
 template <typename T, int VEC, int NR>
-__global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RaArgs a) {
+__global__ void __launch_bounds__(RA_THREADS, NR > 1 ? 12 : 1) rope_append_kernel(const RaArgs a) {
   using V = RaVec<T, VEC>;
-  __shared__ float s_cs[NR][256];
+  __shared__ __align__(16) float s_cs[NR][256];
   __shared__ int64_t s_slot[NR];                     // >= 0 slot offset; -1 a slot without a place; -2 not a node
   const int tid = threadIdx.x;
   const int64_t row0 = int64_t(blockIdx.x) * NR;
@@ -99,10 +103,8 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RaArgs a)
     s_cs[m][h + f] = a.cos_sin[p * a.rot + h + f];
   }
   __syncthreads();
-  const int D = a.c.head_dim, Hk = a.c.heads;
+  const int D = a.c.head_dim, Hk = a.c.heads, H = a.Hq + Hk;
   const int npair = a.interleaved && VEC > 1 ? a.rot / VEC : h / VEC;    // rotated items of a head
-  const int nhead = npair + (D - a.rot) / VEC;                // and those that pass through
-  const int nrope = (a.Hq + Hk) * nhead, nitem = nrope + Hk * (D / VEC);
   const T* q = reinterpret_cast<const T*>(a.q);
   const T* k = reinterpret_cast<const T*>(a.k);
   const T* v = reinterpret_cast<const T*>(a.v);
@@ -110,63 +112,103 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RaArgs a)
   T* kc = reinterpret_cast<T*>(a.c.k);
   T* vc = reinterpret_cast<T*>(a.c.v);
   const int first = blockIdx.y * RA_THREADS + tid, step = gridDim.y * RA_THREADS;
-#pragma unroll
-  for (int m = 0; m < NR; ++m) {
-    const int64_t row = row0 + m;
-    if (row >= a.rows) break;
-    const int64_t at = s_slot[m];
-#pragma unroll 2
-    for (int u = first; u < nitem; u += step) {
-      if (u >= nrope) {                              // values
-        const int x = u - nrope, hd = x / (D / VEC), d = (x - hd * (D / VEC)) * VEC;
-        if (at >= 0)
-          *reinterpret_cast<V*>(vc + at + hd * a.c.head_stride + d) =
-              *reinterpret_cast<const V*>(v + row * a.ldv + int64_t(hd) * D + d);
-        continue;
-      }
-      const int hd = u / nhead, x = u - hd * nhead;
-      const bool isq = hd < a.Hq;
-      if (!isq && at < 0) continue;
-      const T* src = isq ? q + row * a.ldq + int64_t(hd) * D : k + row * a.ldk + int64_t(hd - a.Hq) * D;
-      T* dst = isq ? qo + row * a.ldo + int64_t(hd) * D : kc + at + (hd - a.Hq) * a.c.head_stride;
-      if (at == -2) src = nullptr;
-      if (x >= npair) {                              // columns past the rotated ones
-        const int d = a.rot + (x - npair) * VEC;
-        V y = {};
-        if (src) y = *reinterpret_cast<const V*>(src + d);
-        *reinterpret_cast<V*>(dst + d) = y;
-      } else if (VEC > 1 && a.interleaved) {         // whole pairs side by side
-        const int d = x * VEC;
-        V y = {};
-        if (src) {
-          y = *reinterpret_cast<const V*>(src + d);
-#pragma unroll
-          for (int e = 0; e + 1 < VEC; e += 2) {
-            const float c = s_cs[m][(d + e) / 2], s = s_cs[m][h + (d + e) / 2];
-            const float x1 = ra_f(y.e[e]), x2 = ra_f(y.e[e + 1]);
-            ra_set(y.e[e], __fmaf_rn(x1, c, -__fmul_rn(x2, s)));
-            ra_set(y.e[e + 1], __fmaf_rn(x2, c, __fmul_rn(x1, s)));
-          }
-        }
-        *reinterpret_cast<V*>(dst + d) = y;
-      } else {                                       // the pair's columns d1 and d2
-        const int f = x * VEC, d1 = a.interleaved ? 2 * f : f, d2 = a.interleaved ? 2 * f + 1 : h + f;
-        V y1 = {}, y2 = {};
-        if (src) {
-          y1 = *reinterpret_cast<const V*>(src + d1);
-          y2 = *reinterpret_cast<const V*>(src + d2);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float c = s_cs[m][f + e], s = s_cs[m][h + f + e];
-            const float x1 = ra_f(y1.e[e]), x2 = ra_f(y2.e[e]);
-            ra_set(y1.e[e], __fmaf_rn(x1, c, -__fmul_rn(x2, s)));
-            ra_set(y2.e[e], __fmaf_rn(x2, c, __fmul_rn(x1, s)));
-          }
-        }
-        *reinterpret_cast<V*>(dst + d1) = y1;
-        *reinterpret_cast<V*>(dst + d2) = y2;
+  // walks items (head, x) of `per` a head, `step` apart, without a division each
+  struct Item {
+    int hd, x, per, shd, sx;
+    DS_DEV Item(int at, int per_, int step_) : per(per_) {
+      hd = at / per;
+      x = at - hd * per;
+      shd = step_ / per;
+      sx = step_ - shd * per;
+    }
+    DS_DEV void next() {
+      hd += shd;
+      x += sx;
+      if (x >= per) {
+        x -= per;
+        ++hd;
       }
     }
+  };
+  // "head" hv of the block: head hv % H of its row hv / H (one or two rows)
+  const int rows = int(min(int64_t(NR), a.rows - row0)), heads = rows * H;
+  struct Place {
+    const T* src;              // null: a query of a slot that is no node, which becomes zero
+    T* dst;                    // null: a key without a place, which is not written
+    int m;
+  };
+  auto place = [&](int hv) {
+    Place p;
+    p.m = NR > 1 && hv >= H ? 1 : 0;
+    const int hd = hv - p.m * H;
+    const int64_t row = row0 + p.m, at = s_slot[p.m];
+    if (hd < a.Hq) {
+      p.src = at == -2 ? nullptr : q + row * a.ldq + int64_t(hd) * D;
+      p.dst = qo + row * a.ldo + int64_t(hd) * D;
+    } else {
+      p.src = at < 0 ? nullptr : k + row * a.ldk + int64_t(hd - a.Hq) * D;
+      p.dst = at < 0 ? nullptr : kc + at + (hd - a.Hq) * a.c.head_stride;
+    }
+    return p;
+  };
+  // rotated columns: an item is VEC columns of whole pairs, or both halves' VEC
+  const bool whole = VEC > 1 && a.interleaved;
+  for (Item it(first, npair, step); it.hd < heads; it.next()) {
+    const Place p = place(it.hd);
+    if (!p.dst) continue;
+    const int f = it.x * VEC, d1 = a.interleaved && VEC == 1 ? 2 * f : f, d2 = a.interleaved ? 2 * f + 1 : h + f;
+    V y1 = {}, y2 = {};
+    if (p.src) {
+      y1 = *reinterpret_cast<const V*>(p.src + d1);
+      if (!whole) y2 = *reinterpret_cast<const V*>(p.src + d2);
+    }
+    const float* cs = s_cs[p.m] + (whole ? f / 2 : f);
+    if (whole) {
+#pragma unroll
+      for (int e = 0; e + 1 < VEC; e += 2) {
+        const float c = cs[e / 2], s = cs[h + e / 2];
+        const float x1 = ra_f(y1.e[e]), x2 = ra_f(y1.e[e + 1]);
+        ra_set(y1.e[e], __fmaf_rn(x1, c, -__fmul_rn(x2, s)));
+        ra_set(y1.e[e + 1], __fmaf_rn(x2, c, __fmul_rn(x1, s)));
+      }
+      *reinterpret_cast<V*>(p.dst + d1) = y1;
+    } else {
+      float c[VEC], s[VEC];
+      if constexpr (VEC % 4 == 0) {                    // offsets are multiples of four
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+          *reinterpret_cast<float4*>(c + e) = *reinterpret_cast<const float4*>(cs + e);
+          *reinterpret_cast<float4*>(s + e) = *reinterpret_cast<const float4*>(cs + h + e);
+        }
+      } else {
+        c[0] = cs[0];
+        s[0] = cs[h];
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float x1 = ra_f(y1.e[e]), x2 = ra_f(y2.e[e]);
+        ra_set(y1.e[e], __fmaf_rn(x1, c[e], -__fmul_rn(x2, s[e])));
+        ra_set(y2.e[e], __fmaf_rn(x2, c[e], __fmul_rn(x1, s[e])));
+      }
+      *reinterpret_cast<V*>(p.dst + d1) = y1;
+      *reinterpret_cast<V*>(p.dst + d2) = y2;
+    }
+  }
+  if (a.rot < D) {                                     // columns past the rotated ones
+    for (Item pt(first, (D - a.rot) / VEC, step); pt.hd < heads; pt.next()) {
+      const Place p = place(pt.hd);
+      const int d = a.rot + pt.x * VEC;
+      V y = {};
+      if (p.src) y = *reinterpret_cast<const V*>(p.src + d);
+      if (p.dst) *reinterpret_cast<V*>(p.dst + d) = y;
+    }
+  }
+  for (Item vt(first, D / VEC, step); vt.hd < rows * Hk; vt.next()) {    // values
+    const int m = NR > 1 && vt.hd >= Hk ? 1 : 0, hd = vt.hd - m * Hk;
+    const int64_t at = s_slot[m];
+    if (at >= 0)
+      *reinterpret_cast<V*>(vc + at + hd * a.c.head_stride + vt.x * VEC) =
+          *reinterpret_cast<const V*>(v + (row0 + m) * a.ldv + int64_t(hd) * D + vt.x * VEC);
   }
 }
 

@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     (void)ds_mbar_wait(&s_drain, 0, DS_WAIT_LIMIT);
   } else if (warp < 4) {
     // ---- query rows of each piece into the swizzled layout; columns past head_dim are zero (the key
-    // tile's are too), rows that do not exist keep what was there: a row only reaches its own results ----
+    // tile's are too), rows past the last warp's keep what was there: a row only reaches its own results ----
     constexpr int CPR = DP / 8, STEP = TA_QTHREADS / CPR;        // 16-byte columns of a row, rows per round
     const int qt = lane, c = qt % CPR, D = a.c.head_dim;
     uint32_t np = 0;
@@ -456,6 +456,9 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
         else *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
         for (h += STEP; h >= a.G; h -= a.G) ++i;
       }
+      // rows that only fill up a warp: zeros, whose scores disturb no vote
+      for (int lr = cnt + qt / CPR; lr < min(a.rpg, (cnt + 31) & ~31); lr += STEP)
+        *reinterpret_cast<uint4*>(dst + (lr >> 7) * STAGE + (lr & 127) * 128 + (((c & 7) ^ (lr & 7)) << 4)) = make_uint4(0, 0, 0, 0);
       ds_cp_async_wait_all();
       ds_fence_proxy_async_smem();
       ds_mbar_arrive(&s_qfull);
@@ -752,76 +755,80 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
   }
 }
 
-// Joins the partial results of one row, one warp: the lanes take the parts' maxima and sums (a lane the
-// parts lane, lane + 32, ..), then the columns, adding the parts in the order of the blocks that left
-// them. Rows whose item was finished by one block are left at once.
-template <typename T>
-__global__ void __launch_bounds__(256) tree_attn_join_kernel(const TaArgs a, int32_t grid, int64_t jobs) {
+// Joins the partial results of one row, one warp: 32 parts at a time, a lane takes a part's maximum and sum,
+// then the lanes take the columns and add the parts in the order of the blocks that left them, every load of a
+// part being independent of the others (U = 128-column pieces of a row). Rows whose item was finished by one block are left at once.
+template <typename T, int U>
+__global__ void __launch_bounds__(256) tree_attn_join_kernel(const TaArgs a, uint32_t grid, int64_t jobs) {
   ds_pdl_trigger();
-  ds_pdl_wait();
   const int64_t job = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (job >= jobs) return;
   const int64_t item = ta_div(job, uint32_t(a.rs));
   const int lrow = int(job - item * a.rs);
   const int hm = a.c.heads * a.mg;
   const int r = int(ta_div(item, uint32_t(hm))), sub = int(item - int64_t(r) * hm);
   const int hk = sub / a.mg, g = sub - hk * a.mg, m = g * a.rpg + lrow;
-  const int64_t total = int64_t(a.pref[a.R]) * hm, p0 = a.pref[r], nt = a.pref[r + 1] - p0, g0 = p0 * hm + sub * nt;
-  const uint32_t ut = total > 0xFFFFFFFFll ? 0u : uint32_t(total);
-  auto holder = [&](int64_t tile) {                    // block whose share holds the tile
-    const int64_t x = (tile + 1) * grid + total - 1;
-    return int((ut ? ta_div(x, ut) : x / total) - 1);
-  };
-  const int b0 = holder(g0);
-  if (m >= a.rows || a.start[b0 + 1] >= g0 + nt) return;                // whole
-  const int np = holder(g0 + nt - 1) - b0 + 1;
   const int i = m / a.G, h = hk * a.G + m - i * a.G, D = a.c.head_dim;
   const int64_t row = int64_t(r) * a.T + i;
-  auto part = [&](int k, int64_t& slot) {              // part k: block b0 + k, if its share is not empty
-    const int64_t s0 = a.start[b0 + k];
-    slot = 2 * int64_t(b0 + k) + (s0 > g0 ? 0 : 1);
-    return a.start[b0 + k + 1] > s0;
+  ds_pdl_wait();
+  if (job >= jobs || m >= a.rows) return;
+  const int64_t total = int64_t(__ldcg(a.pref + a.R)) * hm, p0 = __ldcg(a.pref + r), nt = __ldcg(a.pref + r + 1) - p0;
+  const int64_t g0 = p0 * hm + sub * nt;
+  auto start = [&](int64_t b) { return ta_div(total * b, grid); };      // first tile of block b
+  auto holder = [&](int64_t tile) {                    // block whose share holds the tile
+    const int64_t x = (tile + 1) * grid + total - 1;
+    return int((total >> 32 ? ta_div64(x, total) : ta_div(x, uint32_t(total))) - 1);
   };
-  float M = -INFINITY;
-  for (int k = lane; k < np; k += 32) {
-    int64_t slot;
-    if (part(k, slot)) M = fmaxf(M, a.part_ml[slot * a.rs + lrow].x);
-  }
-  M = ds_warp_max(M);
-  float L = 0.0f;
-  float4 o[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-  for (int k0 = 0; k0 < np; k0 += 32) {
-    const int k = k0 + lane;
-    int64_t slot = -1;
-    float w = 0.0f;
-    if (k < np && part(k, slot)) {
-      const float2 ml = a.part_ml[slot * a.rs + lrow];
-      if (ml.y != 0.0f) {                              // something seen (also a sum that is not a number)
-        w = ta_ex2(ml.x - M);
-        L = __fmaf_rn(w, ml.y, L);
-      } else {
-        slot = -1;
-      }
-    } else {
-      slot = -1;
-    }
-    const int cnt = min(32, np - k0);
-#pragma unroll 4
-    for (int e = 0; e < cnt; ++e) {
-      const int64_t se = __shfl_sync(0xFFFFFFFFu, slot, e);
-      const float we = __shfl_sync(0xFFFFFFFFu, w, e);
-      if (se < 0) continue;
-      const float* x = a.part_o + (se * a.rs + lrow) * D;
+  const int b0 = holder(g0);
+  if (start(b0 + 1) >= g0 + nt) return;                // whole
+  const int np = holder(g0 + nt - 1) - b0 + 1;
+  float M = -INFINITY, L = 0.0f;
+  float4 o[U];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int d = lane * 4 + 128 * u;
-        if (d >= D) continue;
-        const float4 y = *reinterpret_cast<const float4*>(x + d);
-        o[u].x = __fmaf_rn(we, y.x, o[u].x);
-        o[u].y = __fmaf_rn(we, y.y, o[u].y);
-        o[u].z = __fmaf_rn(we, y.z, o[u].z);
-        o[u].w = __fmaf_rn(we, y.w, o[u].w);
+  for (int u = 0; u < U; ++u) o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int k0 = 0; k0 < np; k0 += 32) {
+    // part k: what block b0 + k left, if its share is not empty
+    const int64_t s0 = start(b0 + k0 + lane), s1 = start(b0 + k0 + lane + 1);
+    const bool there = k0 + lane < np && s1 > s0;
+    const int32_t slot = 2 * (b0 + k0 + lane) + (s0 > g0 ? 0 : 1);
+    const float2 ml = there ? __ldcg(a.part_ml + int64_t(slot) * a.rs + lrow) : make_float2(-INFINITY, 0.0f);
+    const float before = M;
+    M = fmaxf(M, ds_warp_max(ml.x));
+    const bool seen = ml.y != 0.0f;                    // also a sum that is not a number
+    const float w = seen ? ta_ex2(ml.x - M) : 0.0f, f = before == -INFINITY ? 0.0f : ta_ex2(before - M);
+    L = __fmaf_rn(w, ml.y, L * f);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      o[u].x *= f;
+      o[u].y *= f;
+      o[u].z *= f;
+      o[u].w *= f;
+    }
+    const unsigned live = __ballot_sync(0xFFFFFFFFu, seen);
+    const int cnt = min(32, np - k0);
+    for (int e0 = 0; e0 < cnt; e0 += 8) {
+      float4 y[U][8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t se = __shfl_sync(0xFFFFFFFFu, slot, e0 + e);
+        const float* x = a.part_o + (se * a.rs + lrow) * D;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int d = lane * 4 + 128 * u;
+          y[u][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if ((live >> (e0 + e)) & 1u && d < D) y[u][e] = __ldcg(reinterpret_cast<const float4*>(x + d));
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float we = __shfl_sync(0xFFFFFFFFu, w, e0 + e);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          o[u].x = __fmaf_rn(we, y[u][e].x, o[u].x);
+          o[u].y = __fmaf_rn(we, y[u][e].y, o[u].y);
+          o[u].z = __fmaf_rn(we, y[u][e].z, o[u].z);
+          o[u].w = __fmaf_rn(we, y[u][e].w, o[u].w);
+        }
       }
     }
   }
@@ -830,7 +837,7 @@ __global__ void __launch_bounds__(256) tree_attn_join_kernel(const TaArgs a, int
   const float inv = any ? 1.0f / L : 0.0f;
   T* out = reinterpret_cast<T*>(a.out) + row * a.ldo + int64_t(h) * D;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < U; ++u) {
     const int d = lane * 4 + 128 * u;
     if (d >= D) continue;
     const float y[4] = {any ? o[u].x * inv : 0.0f, any ? o[u].y * inv : 0.0f, any ? o[u].z * inv : 0.0f, any ? o[u].w * inv : 0.0f};
@@ -870,18 +877,17 @@ cudaError_t ta_dispatch_tc(const TaArgs& a, int grid, const CUtensorMap& k, cons
 }
 
 constexpr size_t TA_WS_PREF = 4352;        // pref[TA_MAXR + 1], rounded up to 256 bytes
-inline size_t ta_ws_head(int64_t grid) { return TA_WS_PREF + size_t(ds_ceil_div((grid + 1) * 8, 256) * 256); }
 
 }  // namespace
 
 // Partial results of 2 slots per block: rs rows x (head_dim sums + maximum and sum). rs * head_dim is at
-// most the group's T * cols / heads and at most 256 rows of 256 columns; head_dim >= 8, so the two
-// statistics add at most a quarter.
+// most the group's T * cols / heads, and at most 256 rows of 256 columns (one block per SM) or 64 rows of
+// 256 (the float32 kernel's two blocks); head_dim >= 8, so the two statistics add at most a quarter.
 extern "C" size_t dspark_internal_ws_tree_attention(int64_t R, int32_t T, int64_t cols, int32_t heads) {
   if (R <= 0 || T <= 0 || cols <= 0 || heads <= 0) return 0;
-  const int64_t vals = std::min<int64_t>(int64_t(T) * (cols / heads), 256 * 256);
-  const int64_t slots = 2 * int64_t(ds_num_sms());
-  return ta_ws_head(slots / 2) + size_t(ds_ceil_div(slots * vals * 5, 256) * 256);
+  const int64_t item = int64_t(T) * (cols / heads), sms = ds_num_sms();
+  const int64_t vals = std::max(2 * sms * std::min<int64_t>(item, 256 * 256), 4 * sms * std::min<int64_t>(item, 64 * 256));
+  return TA_WS_PREF + size_t(ds_ceil_div(vals * 5, 256) * 256);
 }
 
 extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64_t R, int32_t T, int32_t Hq,
@@ -913,23 +919,31 @@ extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64
   const bool maps = tc && ta_tensor_map(&mk, cache->k, *cache, box) && ta_tensor_map(&mv, cache->v, *cache, box);
   a.kt = maps ? TA_KT : 64;
   a.box = box;
-  a.rpg = maps ? (a.rows > 128 ? 256 : 128) : 64;
+  if (maps) {
+    a.rpg = a.rows > 128 ? 256 : 128;
+  } else {                                             // groups of 64 rows or fewer, as even as sixteens allow
+    const int64_t groups = ds_ceil_div(a.rows, 64);
+    a.rpg = int32_t(ds_ceil_div(a.rows, groups * 16) * 16);
+  }
   a.mg = int32_t(ds_ceil_div(a.rows, a.rpg));
   a.rs = std::min(a.rows, a.rpg);
   const int64_t jobs = R * cache->heads * int64_t(a.mg) * a.rs;         // rows of all items
   DS_REQUIRE(jobs <= INT32_MAX);
-  const int grid = ds_num_sms();
+  const int grid = ds_num_sms() * (maps || D > 128 ? 1 : 2);
   const int64_t slots = 2 * int64_t(grid);
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   a.pref = reinterpret_cast<int32_t*>(w);
-  a.start = reinterpret_cast<int64_t*>(w + TA_WS_PREF);
-  a.part_o = reinterpret_cast<float*>(w + ta_ws_head(grid));
+  a.part_o = reinterpret_cast<float*>(w + TA_WS_PREF);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * a.rs * D);
   if (maps) DS_CUDA_TRY(D <= 64 ? ta_dispatch_tc<64>(a, grid, mk, mv, stream) : ta_dispatch_tc<128>(a, grid, mk, mv, stream));
   else DS_CUDA_TRY(ta_launch_float(a, grid, stream));
-  if (cache->dtype == DSPARK_BF16)
-    DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<__nv_bfloat16>, dim3(unsigned(ds_ceil_div(jobs, 8))), dim3(256), 0, stream, a, grid, jobs));
-  else
-    DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<float>, dim3(unsigned(ds_ceil_div(jobs, 8))), dim3(256), 0, stream, a, grid, jobs));
+  const dim3 jg{unsigned(ds_ceil_div(jobs, 8))}, jb{256};
+  if (cache->dtype == DSPARK_BF16) {
+    if (D <= 128) DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<__nv_bfloat16, 1>, jg, jb, 0, stream, a, uint32_t(grid), jobs));
+    else DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<__nv_bfloat16, 2>, jg, jb, 0, stream, a, uint32_t(grid), jobs));
+  } else {
+    if (D <= 128) DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<float, 1>, jg, jb, 0, stream, a, uint32_t(grid), jobs));
+    else DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<float, 2>, jg, jb, 0, stream, a, uint32_t(grid), jobs));
+  }
   return DSPARK_OK;
 }

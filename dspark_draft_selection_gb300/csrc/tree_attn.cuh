@@ -25,7 +25,6 @@ struct TaArgs {
   int32_t box;                 // keys per copy (tensor-core kernel)
   float scale, softcap;
   int32_t* pref;               // [R + 1] running sum of the requests' tile counts
-  int64_t* start;              // [blocks + 1] first tile of every block's share
   float2* part_ml;             // [slots][rs] (reference maximum in log2 units, sum)
   float* part_o;               // [slots][rs][D] sums of weights times values, relative to the maximum
   int32_t* status;
@@ -52,6 +51,8 @@ struct TaLens {
   int32_t pref[TA_MAXR + 1], ctx[TA_MAXR], n[TA_MAXR];
   int64_t at, end;
   int32_t r;
+  TaPiece first;               // the share's first piece, which next() would find
+  int32_t any;                 // whether there is one
 };
 
 // Quotient of a number that rarely needs more than 32 bits (the long division stays out of line).
@@ -63,12 +64,22 @@ DS_DEV int64_t ta_div(int64_t x, uint32_t d) {
 struct TaWalk {
   int64_t at, end;
   int32_t r;
+  bool begun;
   DS_DEV void init(const TaLens& s) {
     at = s.at;
     end = s.end;
     r = s.r;
+    begun = false;
   }
+  // The next piece of the share; the first one was found once for all warps.
   DS_DEV bool next(const TaLens& s, const TaArgs& a, TaPiece& p) {
+    if (begun) return find(s, a, p);
+    begun = true;
+    p = s.first;
+    at += p.t1 - p.t0;
+    return s.any != 0;
+  }
+  DS_DEV bool find(const TaLens& s, const TaArgs& a, TaPiece& p) {
     if (at >= end) return false;
     const int64_t hm = int64_t(a.c.heads) * a.mg;
     while (s.pref[r + 1] * hm <= at) ++r;
@@ -86,8 +97,8 @@ struct TaWalk {
 };
 
 // Lengths and running tile counts by all threads of the block. A length or node count out of range is
-// reported and cut so that no slot past the page table is read. Block 0 leaves the counts and every
-// block's first tile for the join.
+// reported and cut so that no slot past the page table is read. Block 0 leaves the counts for the
+// join.
 DS_DEV void ta_prefix(const TaArgs& a, TaLens& s) {
   const int tid = threadIdx.x;
   const int64_t cap = int64_t(a.c.table_pages) * a.c.page_size;
@@ -136,18 +147,23 @@ DS_DEV void ta_prefix(const TaArgs& a, TaLens& s) {
       if (before) r = r0 + 31 - __clz(int(before));
       if (before != 0xFFFFFFFFu) break;
     }
+    TaWalk w;
+    w.at = at;
+    w.end = ta_div(total * (blockIdx.x + 1), gridDim.x);
+    w.r = r;
+    TaPiece p = {};
+    const bool any = w.find(s, a, p);
     if (tid == 0) {
       s.at = at;
-      s.end = ta_div(total * (blockIdx.x + 1), gridDim.x);
+      s.end = w.end;
       s.r = r;
+      s.first = p;
+      s.any = any;
     }
   }
   __syncthreads();
-  if (blockIdx.x == 0) {
+  if (blockIdx.x == 0)
     for (int r = tid; r <= a.R; r += blockDim.x) a.pref[r] = s.pref[r];
-    const int64_t total = s.pref[a.R] * (int64_t(a.c.heads) * a.mg);
-    for (int b = tid; b <= int(gridDim.x); b += blockDim.x) a.start[b] = ta_div(total * b, gridDim.x);
-  }
 }
 
 // Bits of the 32 keys whose first is node `nd` (negative: committed slots, which every node sees),

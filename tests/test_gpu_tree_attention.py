@@ -134,6 +134,25 @@ def test_maxima_that_keep_rising(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("softcap", [0.0, 200.0])
+@pytest.mark.parametrize("T,Hq", [(4, 4), (90, 4)])        # one tile of rows, two
+def test_maxima_that_leap(dtype, softcap, T, Hq):
+    """Scores that jump by tens and hundreds of log2 units from one key to the next, at the places in a tile and
+    in the order where the reference of the weights has to follow, and that fall as far again."""
+    c = Case(6, T, Hq, 2, 64, 32, [1500], None, dtype, mask="chain", scale=0.25, softcap=softcap)
+    c.q[:] = c.q.sign() * 0.5                                # every query's score of a key along its own signs is large
+    s = torch.arange(1500, device="cuda")
+    at = c.table[0].long()[s // 32], s % 32
+    c.k[at] = (c.k[at].float() * 0.05).to(c.k.dtype)
+    for j, size in ((5, 8.0), (40, -30.0), (131, 20.0), (140, 40.0), (255, 45.0), (256, 70.0), (300, 75.0), (383, 10.0),
+                    (640, 130.0), (655, 190.0), (700, 60.0), (1279, 191.0), (1290, -200.0)):
+        i = (j * 7) % T                                      # along another node's query each time
+        for h in range(2):
+            c.k[c.table[0].long()[j // 32], j % 32, h] = (c.q[0, i, h * (Hq // 2)].float() * size / 4).to(c.k.dtype)
+    c.run().check(rows=None if T < 10 else [(j * 7) % T for j in (5, 131, 255, 256, 640, 655, 1279)] + [0, 1, T - 1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("junk", [float("nan"), float("inf"), -float("inf"), 3e38])
 @pytest.mark.parametrize("T,ctx", [(11, 100), (70, 190), (40, 88)])
 def test_what_is_not_seen_has_no_effect(dtype, junk, T, ctx):
