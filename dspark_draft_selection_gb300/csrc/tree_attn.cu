@@ -31,6 +31,7 @@ constexpr int TA_THREADS = 384;
 constexpr int TA_QTHREADS = 32;
 constexpr uint32_t TA_CHUNK = 128 * 128;   // bytes of 128 rows x 64 bf16 columns
 constexpr float TA_RISE = 8.0f;            // log2 rise of the maximum that rescales O
+constexpr float TA_FIXED = 80.0f;          // caps (log2) up to which the reference stays 0
 
 template <int DP, bool TWO>
 __host__ __device__ constexpr int ta_stages() {
@@ -129,34 +130,23 @@ DS_DEV void ta_arrived(float (&v)[16]) {
 // cap2 * tanh(sy * s) = s * Q(s^2): tanh(y) = y P(y^2) with the coefficients of P that make the largest
 // relative error smallest (fitted by reweighted least squares), scaled by the powers of sy and by cap2; two
 // values at a time. Seven coefficients serve |y| <= 1 and four |y| <= 0.375; as evaluated in float32 their
-// errors are 1.6e-7 and 1.5e-7.
-struct TaTanhPoly {
-  float c[7], d[4];
-  DS_DEV TaTanhPoly(float sy, float cap2) {
-    const float p[7] = {0x1.fffffep-1f, -0x1.55540ap-2f, 0x1.10e672p-3f, -0x1.b5eb8p-5f, 0x1.4c6e4ap-6f, -0x1.968b3ap-8f, 0x1.10e592p-10f};
-    const float q[4] = {0x1.fffffep-1f, -0x1.5551c6p-2f, 0x1.10110cp-3f, -0x1.8b7242p-5f};
-    float f = sy * cap2;
+// errors are 1.6e-7 and 1.5e-7. The scaled coefficients are kernel arguments (a pair of each), made by
+// ta_tanh_coefficients.
+DS_DEV uint64_t ta_pair(float2 x) { return ds_f2(x.x, x.y); }
+DS_DEV uint64_t ta_poly_wide(const TaArgs& a, uint64_t s) {
+  const uint64_t u = ds_fma2(s, s, 0);
+  uint64_t q = ta_pair(a.wide[6]);
 #pragma unroll
-    for (int k = 0; k < 7; ++k, f *= sy * sy) {
-      c[k] = p[k] * f;
-      if (k < 4) d[k] = q[k] * f;
-    }
-  }
-  DS_DEV uint64_t wide(uint64_t s) const {
-    const uint64_t u = ds_fma2(s, s, 0);
-    uint64_t q = ds_f2(c[6], c[6]);
+  for (int k = 5; k >= 0; --k) q = ds_fma2(q, u, ta_pair(a.wide[k]));
+  return q;
+}
+DS_DEV uint64_t ta_poly_narrow(const TaArgs& a, uint64_t s) {
+  const uint64_t u = ds_fma2(s, s, 0);
+  uint64_t q = ta_pair(a.narrow[3]);
 #pragma unroll
-    for (int k = 5; k >= 0; --k) q = ds_fma2(q, u, ds_f2(c[k], c[k]));
-    return q;
-  }
-  DS_DEV uint64_t narrow(uint64_t s) const {
-    const uint64_t u = ds_fma2(s, s, 0);
-    uint64_t q = ds_f2(d[3], d[3]);
-#pragma unroll
-    for (int k = 2; k >= 0; --k) q = ds_fma2(q, u, ds_f2(d[k], d[k]));
-    return q;
-  }
-};
+  for (int k = 2; k >= 0; --k) q = ds_fma2(q, u, ta_pair(a.narrow[k]));
+  return q;
+}
 
 // High word of both layouts: groups of eight rows (K-major: query or key rows; N-major: keys) 1024 bytes
 // apart, descriptor version 1, 128-byte swizzle. Low words: K-major needs no leading offset; an operand
@@ -471,7 +461,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     const uint32_t tS = tl + TS + 128 * g, tO = tl + TO + DP * g;
     const float sc = CAP ? a.scale * 2.0f * TA_LOG2E / a.softcap : a.scale * TA_LOG2E;
     const float cap2 = a.softcap * TA_LOG2E, sy = CAP ? a.scale / a.softcap : 0.0f;
-    const TaTanhPoly tanh_poly(sy, cap2);
+    const bool fixed = CAP && cap2 <= TA_FIXED;                // the reference stays 0
     const int D = a.c.head_dim;
     uint32_t np = 0, ns = 0, seq = 0;
     bool first = true, ok = true;
@@ -482,7 +472,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
       const int m = p.g * a.rpg + (TWO ? g * 128 : 0) + lr;    // this thread's row
       const bool live = p.g * a.rpg + (TWO ? g * 128 : 0) + quarter * 32 < a.rows;   // any row of this warp
       const int i = min(m, a.rows - 1) / a.G;
-      float mref = -INFINITY, l = 0.0f;
+      float mref = fixed ? 0.0f : -INFINITY, l = 0.0f;         // reference (log2) and sum of this thread's row
       bool has = false;                                        // O holds an earlier tile
       for (int t = TWO ? 0 : g; t < npt; t += TWO ? 1 : 2) {
         ok = wait(&s_sfull[g], ns++, first ? a.first_wait : DS_WAIT_LIMIT);
@@ -535,6 +525,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) mg4[(e >> 1) & 3] = fmaxf(mg4[(e >> 1) & 3], fmaxf(fabsf(v[e]), fabsf(v[e + 1])));
               }
+              if (CAP && fixed) return;
               if (CAP && masked) {
                 const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 32 * c);
 #pragma unroll
@@ -559,6 +550,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           const float mg = fmaxf(fmaxf(mg4[0], mg4[1]), fmaxf(mg4[2], mg4[3]));
           float v[16];
           ta_tmem_fetch(tS, v);
+          // Under a cap the exponents stay within +-cap log2(e); up to TA_FIXED that fits the range of the
+          // weights, their sums and O (2^80 x 2^17 keys x the values), so no maximum is needed.
           const float m2 = mx == -INFINITY ? -INFINITY : CAP ? ta_tanh(mx * sc, cap2) : mx * sc;
           const bool up = m2 > mref + TA_RISE || (mref == -INFINITY && m2 > -INFINITY);
           if (__any_sync(0xFFFFFFFFu, up)) {
@@ -597,7 +590,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const uint64_t y = ds_f2(v[2 * e], v[2 * e + 1]);
-              x[e] = ds_fma2(y, CAP ? tanh_poly.narrow(y) : ds_f2(sc, sc), nm2);
+              x[e] = ds_fma2(y, CAP ? ta_poly_narrow(a, y) : ds_f2(sc, sc), nm2);
             }
           };
           if (!CAP || (narrow && !masked)) {
@@ -626,7 +619,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                   const uint64_t y = ds_f2(v[2 * e], v[2 * e + 1]);
-                  x[e] = ds_fma2(y, tanh_poly.wide(y), nm2);
+                  x[e] = ds_fma2(y, ta_poly_wide(a, y), nm2);
                 }
               } else {
 #pragma unroll
@@ -876,6 +869,18 @@ cudaError_t ta_dispatch_tc(const TaArgs& a, int grid, const CUtensorMap& k, cons
   return a.softcap > 0.0f ? ta_launch_tc<DP, false, true>(a, grid, k, v, st) : ta_launch_tc<DP, false, false>(a, grid, k, v, st);
 }
 
+void ta_tanh_coefficients(TaArgs& a, float scale, float cap) {
+  static const double p[7] = {0x1.fffffep-1, -0x1.55540ap-2, 0x1.10e672p-3, -0x1.b5eb8p-5, 0x1.4c6e4ap-6, -0x1.968b3ap-8, 0x1.10e592p-10};
+  static const double q[4] = {0x1.fffffep-1, -0x1.5551c6p-2, 0x1.10110cp-3, -0x1.8b7242p-5};
+  if (!(cap > 0.0f)) return;
+  const double sy = double(scale) / cap;
+  double f = sy * cap * 1.4426950408889634;
+  for (int k = 0; k < 7; ++k, f *= sy * sy) {
+    a.wide[k] = make_float2(float(p[k] * f), float(p[k] * f));
+    if (k < 4) a.narrow[k] = make_float2(float(q[k] * f), float(q[k] * f));
+  }
+}
+
 constexpr size_t TA_WS_PREF = 4352;        // pref[TA_MAXR + 1], rounded up to 256 bytes
 
 }  // namespace
@@ -907,6 +912,7 @@ extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64
   TaArgs a{};
   a.q = q; a.ldq = ldq; a.out = out; a.ldo = ldo; a.lse = lse; a.c = *cache; a.ctx_len = ctx_len; a.n_nodes = n_nodes;
   a.mask = mask; a.R = int32_t(R); a.T = T; a.Hq = Hq; a.G = Hq / cache->heads; a.W = (T + 31) / 32;
+  ta_tanh_coefficients(a, scale, softcap);
   a.rows = T * a.G; a.scale = scale; a.softcap = softcap; a.status = dev_status; a.first_wait = g_ds_first_wait_polls.load();
   int box = 128;
   while (cache->page_size % box) box >>= 1;

@@ -24,6 +24,7 @@ struct TaArgs {
   int32_t kt;                  // keys per tile
   int32_t box;                 // keys per copy (tensor-core kernel)
   float scale, softcap;
+  float2 wide[7], narrow[4];   // coefficients of the cap's polynomials, each twice
   int32_t* pref;               // [R + 1] running sum of the requests' tile counts
   float2* part_ml;             // [slots][rs] (reference maximum in log2 units, sum)
   float* part_o;               // [slots][rs][D] sums of weights times values, relative to the maximum
