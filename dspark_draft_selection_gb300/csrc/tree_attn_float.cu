@@ -2,14 +2,17 @@
 // that the tensor-core kernel does not take (head_dim above 128, pages that are no multiple of eight
 // places, rows off 16-byte boundaries).
 //
-// One block of 256 threads works through its share of the line of tiles (tree_attn.cuh) with up to 64 query
-// rows and 64 keys at a time. A thread holds RPT rows x 4 scores, then RPT rows x 2 UC columns of the result
-// (RPT = 1..4, the least that covers the rows of a (request, key head); UC = head_dim / 32 rounded up), the
-// row statistics being reduced over the 16 lanes that share a row. Keys and values stay in their own type in
-// shared memory and are copied asynchronously, the values while the scores are computed; the weights take the
-// keys' place. So two blocks fit an SM (head_dim <= 128) and one computes while the other waits for its
-// copies. Bound by the FMA rate: 4 head_dim operations per query row and key, far above what HBM needs.
-// Six requests of 13 nodes x 3 heads, 80 columns, up to 1,500 keys: FIGURE.
+// One block of eight warps works through its share of the line of tiles (tree_attn.cuh) with up to 64 query
+// rows and 64 keys at a time. A warp owns RW rows (2, 4, 6 or 8, the least that covers the rows of a (request,
+// key head)); its lanes are keys for the scores (two each) and columns for the result (UC = head_dim / 32
+// rounded up), so a warp's weights are its own and need no block-wide barrier. Keys and values stay in their
+// own type in shared memory and are copied asynchronously, the values while the scores are computed; the
+// weights take the keys' place. Two blocks fit an SM (head_dim <= 128): one computes while the other waits.
+// Bound by what shared memory returns to registers - RW + 2 values for 2 RW FMAs of the scores - and, where
+// a block has one tile, by the latency of its phases. Six requests of 13 nodes x 3 heads, 80 columns and up
+// to 1,500 keys (one tile a block): FIGURE.
+#include <type_traits>
+
 #include "tree_attn.cuh"
 
 namespace {
@@ -18,7 +21,7 @@ constexpr int TF_KEYS = 64;
 constexpr int TF_THREADS = 256;
 constexpr int TF_LDP = TF_KEYS + 4;
 
-// Shared memory: RPT * 16 query rows as float32; the key tile, whose place the weights take; the value tile.
+// Shared memory: 8 RW query rows as float32; the key tile, whose place the weights take; the value tile.
 template <typename T>
 struct TfLayout {
   int ldq, ldk, ldv;           // elements of a row
@@ -40,11 +43,6 @@ DS_DEV float4 tf_4(const __nv_bfloat16* p) {
   const uint2 u = *reinterpret_cast<const uint2*>(p);
   return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
                      __uint_as_float(u.y & 0xFFFF0000u));
-}
-DS_DEV float2 tf_2(const float* p) { return *reinterpret_cast<const float2*>(p); }
-DS_DEV float2 tf_2(const __nv_bfloat16* p) {
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
 }
 DS_DEV void tf_put(float* p, float x) { *p = x; }
 DS_DEV void tf_put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
@@ -71,24 +69,16 @@ DS_DEV void tf_copy(T* dst, int ld, const T* src, const int64_t* s_at, int D, bo
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-DS_DEV float tf_rowmax(float x) {
-#pragma unroll
-  for (int d = 8; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
-  return x;
-}
-DS_DEV float tf_rowsum(float x) {
-#pragma unroll
-  for (int d = 8; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-  return x;
-}
+// A capped score in units of log2 (out of line: the code of a tile, which short contexts run once, stays small).
+__device__ __noinline__ float tf_capped(float s, float scale, float cap) { return cap * tanhf(s * scale / cap) * TA_LOG2E; }
 
-template <typename T, int RPT, int UC>
-__global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const TaArgs a, bool veckv) {
+template <typename T, int RW, int UC>
+__global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const TaArgs a, bool vecq, bool veckv) {
   extern __shared__ uint4 smem4[];
   __shared__ TaLens s_len;
   __shared__ int64_t s_at[TF_KEYS];
-  const int D = a.c.head_dim, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const TfLayout<T> lay(D, RPT * 16);
+  const int D = a.c.head_dim, tid = threadIdx.x, lane = tid & 31, row0 = (tid >> 5) * RW;
+  const TfLayout<T> lay(D, RW * 8);
   uint8_t* base = reinterpret_cast<uint8_t*>(smem4);
   float* sQ = reinterpret_cast<float*>(base);
   T* sK = reinterpret_cast<T*>(base + lay.q);
@@ -112,24 +102,31 @@ __global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const Ta
       return t < p.t1 && key < len ? ta_slot(a, p.r, key) : int64_t(-1);
     };
     int64_t mine = tid < TF_KEYS ? slot_of(p.t0) : -1;
-    for (int u = tid; u < RPT * 16 * D; u += TF_THREADS) {
-      const int lr = u / D, d = u - lr * D, m = m0 + lr;
-      float x = 0.0f;
-      if (m < a.rows) {
-        const int i = m / a.G;
-        x = ds_load_elem<T>(q + (int64_t(p.r) * a.T + i) * a.ldq + int64_t(p.hk * a.G + m - i * a.G) * D + d);
+    {                                                // query rows, widened; four columns and row after row a thread
+      const int per = D / 4, step = TF_THREADS / per, c = tid % per;
+      const T* qr = q + int64_t(p.r) * a.T * a.ldq + int64_t(p.hk) * a.G * D + c * 4;
+      int lr = tid / per, i = (m0 + lr) / a.G, h = (m0 + lr) - i * a.G;
+#pragma unroll 4
+      for (; lr < RW * 8; lr += step) {
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (tid < per * step && m0 + lr < a.rows) {
+          const T* at = qr + int64_t(i) * a.ldq + h * D;
+          x = vecq ? tf_4(at)
+                   : make_float4(ds_load_elem<T>(at), ds_load_elem<T>(at + 1), ds_load_elem<T>(at + 2), ds_load_elem<T>(at + 3));
+        }
+        if (tid < per * step) *reinterpret_cast<float4*>(sQ + lr * lay.ldq + c * 4) = x;
+        for (h += step; h >= a.G; h -= a.G) ++i;
       }
-      sQ[lr * lay.ldq + d] = x;
     }
-    float mref[RPT], l[RPT], o[RPT][2 * UC];
-    int node[RPT];
+    float mref[RW], l[RW], o[RW][UC];
+    int node[RW];
 #pragma unroll
-    for (int x = 0; x < RPT; ++x) {
+    for (int x = 0; x < RW; ++x) {
       mref[x] = -INFINITY;
       l[x] = 0.0f;
-      node[x] = min(m0 + ty * RPT + x, a.rows - 1) / a.G;
+      node[x] = min(m0 + row0 + x, a.rows - 1) / a.G;
 #pragma unroll
-      for (int c = 0; c < 2 * UC; ++c) o[x][c] = 0.0f;
+      for (int c = 0; c < UC; ++c) o[x][c] = 0.0f;
     }
     for (int t = p.t0; t < p.t1; ++t) {
       const int64_t key0 = int64_t(t) * TF_KEYS;
@@ -140,134 +137,139 @@ __global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const Ta
       mine = tid < TF_KEYS ? slot_of(t + 1) : -1;
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();
-      float s[RPT][4] = {};
+      float s[RW][2] = {};
+#pragma unroll 1
       for (int d = 0; d < D; d += 4) {
-        float4 kx[4];
+        const float4 k0 = tf_4(sK + lane * lay.ldk + d), k1 = tf_4(sK + (lane + 32) * lay.ldk + d);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) kx[b] = tf_4(sK + (tx + 16 * b) * lay.ldk + d);
-#pragma unroll
-        for (int x = 0; x < RPT; ++x) {
-          const float4 qx = tf_4(sQ + (ty * RPT + x) * lay.ldq + d);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            s[x][b] = __fmaf_rn(qx.x, kx[b].x, s[x][b]);
-            s[x][b] = __fmaf_rn(qx.y, kx[b].y, s[x][b]);
-            s[x][b] = __fmaf_rn(qx.z, kx[b].z, s[x][b]);
-            s[x][b] = __fmaf_rn(qx.w, kx[b].w, s[x][b]);
-          }
+        for (int x = 0; x < RW; ++x) {
+          const float4 qx = tf_4(sQ + (row0 + x) * lay.ldq + d);
+          s[x][0] = __fmaf_rn(qx.x, k0.x, s[x][0]);
+          s[x][1] = __fmaf_rn(qx.x, k1.x, s[x][1]);
+          s[x][0] = __fmaf_rn(qx.y, k0.y, s[x][0]);
+          s[x][1] = __fmaf_rn(qx.y, k1.y, s[x][1]);
+          s[x][0] = __fmaf_rn(qx.z, k0.z, s[x][0]);
+          s[x][1] = __fmaf_rn(qx.z, k1.z, s[x][1]);
+          s[x][0] = __fmaf_rn(qx.w, k0.w, s[x][0]);
+          s[x][1] = __fmaf_rn(qx.w, k1.w, s[x][1]);
         }
       }
       __syncthreads();                               // the keys make room for the weights
       const bool masked = key0 + TF_KEYS > ctx;
 #pragma unroll
-      for (int x = 0; x < RPT; ++x) {
-        uint32_t bits[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      for (int x = 0; x < RW; ++x) {
+        bool seen[2] = {true, true};
         if (masked) {
-          bits[0] = ta_mask32(a, p.r, node[x], n, key0 - ctx);
-          bits[1] = ta_mask32(a, p.r, node[x], n, key0 + 32 - ctx);
-        }
-        float mx = -INFINITY;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {                // scores in units of log2, like the reference maximum
-          s[x][b] = a.softcap > 0.0f ? a.softcap * tanhf(s[x][b] * a.scale / a.softcap) * TA_LOG2E : s[x][b] * (a.scale * TA_LOG2E);
-          if (!((bits[b >> 1] >> (tx + 16 * (b & 1))) & 1u)) s[x][b] = -INFINITY;
-          mx = fmaxf(mx, s[x][b]);
+          for (int b = 0; b < 2; ++b) seen[b] = (ta_mask32(a, p.r, node[x], n, key0 + 32 * b - ctx) >> lane) & 1u;
         }
-        const float mn = fmaxf(mref[x], tf_rowmax(mx));
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {                // scores in units of log2, like the reference maximum
+          s[x][b] = a.softcap > 0.0f ? tf_capped(s[x][b], a.scale, a.softcap) : s[x][b] * (a.scale * TA_LOG2E);
+          if (!seen[b]) s[x][b] = -INFINITY;
+        }
+        const float mn = fmaxf(mref[x], ds_warp_max(fmaxf(s[x][0], s[x][1])));
         const float f = mref[x] == -INFINITY ? 0.0f : exp2f(mref[x] - mn), mu = mn == -INFINITY ? 0.0f : mn;
         mref[x] = mn;
-        float sum = 0.0f;
+        const float w0 = exp2f(s[x][0] - mu), w1 = exp2f(s[x][1] - mu);
+        sP[(row0 + x) * TF_LDP + lane] = seen[0] ? w0 : -1.0f;           // -1: not seen
+        sP[(row0 + x) * TF_LDP + lane + 32] = seen[1] ? w1 : -1.0f;
+        l[x] = __fmaf_rn(l[x], f, ds_warp_sumf((seen[0] ? w0 : 0.0f) + (seen[1] ? w1 : 0.0f)));
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const bool seen = (bits[b >> 1] >> (tx + 16 * (b & 1))) & 1u;
-          const float w = exp2f(s[x][b] - mu);
-          sum += seen ? w : 0.0f;
-          sP[(ty * RPT + x) * TF_LDP + tx + 16 * b] = seen ? w : -1.0f;   // -1: not seen
-        }
-        l[x] = __fmaf_rn(l[x], f, tf_rowsum(sum));
-#pragma unroll
-        for (int c = 0; c < 2 * UC; ++c) o[x][c] *= f;
+        for (int c = 0; c < UC; ++c) o[x][c] *= f;
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
-      auto add = [&](bool some) {                    // some: nodes among the keys that a row may not see
-        for (int j = 0; j < TF_KEYS; j += 4) {
-          float4 w[RPT];
+      // What a row does not see has no effect on it, whatever it is: with a value that is not finite in a tile
+      // that holds nodes, every weight is looked at; else an unseen key's weight counts as 0.
+      bool odd = false;
+      if (masked) {
+        for (int u = tid; u < TF_KEYS * (D / 4); u += TF_THREADS) {      // the rows lie one after the other
+          const float4 y = tf_4(sV + u * 4);
+          odd = odd || !(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY);
+        }
+        odd = __syncthreads_or(odd);
+      }
+      const int keys = int(min(int64_t(TF_KEYS), (len - key0 + 3) & ~int64_t(3)));   // past them all weights are -1
+      auto add = [&](auto mode) {                    // 0: all seen, 1: unseen keys among them, 2: odd values too
+        constexpr int MODE = decltype(mode)::value;
+#pragma unroll 1
+        for (int j = 0; j < keys; j += 4) {
+          float w[RW][4];
 #pragma unroll
-          for (int x = 0; x < RPT; ++x) w[x] = tf_4(sP + (ty * RPT + x) * TF_LDP + j);
+          for (int x = 0; x < RW; ++x) {
+            const float4 y = tf_4(sP + (row0 + x) * TF_LDP + j);
+            w[x][0] = y.x; w[x][1] = y.y; w[x][2] = y.z; w[x][3] = y.w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (MODE == 1 && w[x][e] < 0.0f) w[x][e] = 0.0f;
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
 #pragma unroll
             for (int u = 0; u < UC; ++u) {
-              const int d = tx * 2 + 32 * u;
-              if (d >= D) break;
-              const float2 y = tf_2(sV + (j + e) * lay.ldv + d);
+              const float y = ds_load_elem<T>(sV + (j + e) * lay.ldv + min(lane + 32 * u, D - 1));
 #pragma unroll
-              for (int x = 0; x < RPT; ++x) {
-                const float we = e == 0 ? w[x].x : e == 1 ? w[x].y : e == 2 ? w[x].z : w[x].w;
-                if (some && we < 0.0f) continue;     // what the row does not see has no effect, whatever it is
-                o[x][2 * u] = __fmaf_rn(we, y.x, o[x][2 * u]);
-                o[x][2 * u + 1] = __fmaf_rn(we, y.y, o[x][2 * u + 1]);
+              for (int x = 0; x < RW; ++x) {
+                if (MODE == 2 && w[x][e] < 0.0f) continue;
+                o[x][u] = __fmaf_rn(w[x][e], y, o[x][u]);
               }
             }
           }
         }
       };
-      if (masked) add(true);
-      else add(false);
+      if (!masked) add(std::integral_constant<int, 0>{});
+      else if (!odd) add(std::integral_constant<int, 1>{});
+      else add(std::integral_constant<int, 2>{});
     }
     const bool whole = p.whole();
     const int64_t slot = p.slot(blockIdx.x);
 #pragma unroll
-    for (int x = 0; x < RPT; ++x) {
-      const int lr = ty * RPT + x, m = m0 + lr;
+    for (int x = 0; x < RW; ++x) {
+      const int lr = row0 + x, m = m0 + lr;
       if (lr >= a.rpg || m >= a.rows) break;
       const int i = m / a.G, h = p.hk * a.G + m - i * a.G;
       const bool valid = i < n, any = valid && l[x] != 0.0f;
       const int64_t row = int64_t(p.r) * a.T + i;
       const float inv = any ? 1.0f / l[x] : 0.0f;
-      if (tx == 0) {
+      if (lane == 0) {
         if (!whole) a.part_ml[slot * a.rs + lr] = valid ? make_float2(mref[x], l[x]) : make_float2(-INFINITY, 0.0f);
         else if (a.lse) a.lse[row * a.Hq + h] = any ? (mref[x] + log2f(l[x])) * TA_LN2 : -INFINITY;
       }
 #pragma unroll
       for (int u = 0; u < UC; ++u) {
-        const int d = tx * 2 + 32 * u;
+        const int d = lane + 32 * u;
         if (d >= D) break;
-        if (!whole) {
-          *reinterpret_cast<float2*>(a.part_o + (slot * a.rs + lr) * D + d) = make_float2(o[x][2 * u], o[x][2 * u + 1]);
-        } else {
-          T* out = reinterpret_cast<T*>(a.out) + row * a.ldo + int64_t(h) * D + d;
-          tf_put(out, any ? o[x][2 * u] * inv : 0.0f);
-          tf_put(out + 1, any ? o[x][2 * u + 1] * inv : 0.0f);
-        }
+        if (!whole) a.part_o[(slot * a.rs + lr) * D + d] = o[x][u];
+        else tf_put(reinterpret_cast<T*>(a.out) + row * a.ldo + int64_t(h) * D + d, any ? o[x][u] * inv : 0.0f);
       }
     }
   }
 }
 
-template <typename T, int RPT, int UC>
+template <typename T, int RW, int UC>
 cudaError_t tf_launch(const TaArgs& a, int grid, cudaStream_t st) {
-  const size_t smem = TfLayout<T>(a.c.head_dim, RPT * 16).total();
-  const cudaError_t e = ds_ensure_smem(reinterpret_cast<const void*>(tree_attn_float_kernel<T, RPT, UC>), smem);
+  const size_t smem = TfLayout<T>(a.c.head_dim, RW * 8).total();
+  const cudaError_t e = ds_ensure_smem(reinterpret_cast<const void*>(tree_attn_float_kernel<T, RW, UC>), smem);
   if (e != cudaSuccess) return e;
-  return ds_launch(tree_attn_float_kernel<T, RPT, UC>, dim3(unsigned(grid)), dim3(TF_THREADS), smem, st, a, ds_cache_vec(&a.c));
+  return ds_launch(tree_attn_float_kernel<T, RW, UC>, dim3(unsigned(grid)), dim3(TF_THREADS), smem, st, a,
+                   ds_aligned(a.q, 16) && (a.ldq * int64_t(sizeof(T))) % 16 == 0, ds_cache_vec(&a.c));
 }
 
-template <typename T, int RPT>
+template <typename T, int RW>
 cudaError_t tf_columns(const TaArgs& a, int grid, cudaStream_t st) {
   const int D = a.c.head_dim;
-  return D <= 64 ? tf_launch<T, RPT, 2>(a, grid, st) : D <= 96 ? tf_launch<T, RPT, 3>(a, grid, st)
-       : D <= 128 ? tf_launch<T, RPT, 4>(a, grid, st) : tf_launch<T, RPT, 8>(a, grid, st);
+  return D <= 64 ? tf_launch<T, RW, 2>(a, grid, st) : D <= 96 ? tf_launch<T, RW, 3>(a, grid, st)
+       : D <= 128 ? tf_launch<T, RW, 4>(a, grid, st) : tf_launch<T, RW, 8>(a, grid, st);
 }
 
 template <typename T>
 cudaError_t tf_rows(const TaArgs& a, int grid, cudaStream_t st) {
   switch (ds_ceil_div(a.rpg, 16)) {
-    case 1: return tf_columns<T, 1>(a, grid, st);
-    case 2: return tf_columns<T, 2>(a, grid, st);
-    case 3: return tf_columns<T, 3>(a, grid, st);
-    default: return tf_columns<T, 4>(a, grid, st);
+    case 1: return tf_columns<T, 2>(a, grid, st);
+    case 2: return tf_columns<T, 4>(a, grid, st);
+    case 3: return tf_columns<T, 6>(a, grid, st);
+    default: return tf_columns<T, 8>(a, grid, st);
   }
 }
 
