@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -422,36 +423,47 @@ def dspark_verify(tgt_logits, B, draft_tgt, n_draft, q, *, V_q=None, q_d2t=None,
     return out + (status,)
 
 
+_KV = struct.Struct("@" + "".join({c_vp: "P", c_i32: "i", c_i64: "q"}[t] for _, t in KVCache._fields_))
+_I32 = torch.int32
+
+
 def _kvcache(k, v, page_table):
-    """KVCache of k, v [(layers,) pages, page, heads, head_dim] (any strides, the last 1) and page_table [R, n]."""
-    shape, st = k.shape, k.stride()
-    if v.shape != shape or v.stride() != st or v.dtype != k.dtype:
+    """(bytes of a dspark_kvcache, heads, head_dim, requests) of k, v [(layers,) pages, page, heads, head_dim] (any
+    strides, the last 1) and page_table [R, n]. Packed bytes cost a third of filling a ctypes structure."""
+    sh, st = k.shape, k.stride()
+    if v.shape != sh or v.stride() != st or v.dtype is not k.dtype:
         raise ValueError("keys and values are of one shape, layout and type")
-    if len(shape) not in (4, 5) or st[-1] != 1:
+    n = len(st)
+    if n not in (4, 5) or st[-1] != 1:
         raise ValueError("expected [(layers,) pages, page, heads, head_dim] with unit column stride")
-    if page_table.dim() != 2 or page_table.stride(1) != 1 or page_table.dtype != torch.int32:
+    tsh, tst = page_table.shape, page_table.stride()
+    if len(tsh) != 2 or tst[1] != 1 or page_table.dtype is not _I32:
         raise ValueError("expected an int32 page table [R, pages] with unit column stride")
-    layers, lst = (shape[0], st[0]) if len(shape) == 5 else (1, 0)
-    return KVCache(_p(k), _p(v), _dt(k), layers, lst, st[-4], st[-3], st[-2], shape[-4], shape[-3], shape[-2], shape[-1],
-                   _p(page_table), max(page_table.stride(0), page_table.shape[1]), page_table.shape[1])
+    R, entries = tsh
+    pages, page, H, D = sh[-4:]
+    layers, lst = (sh[0], st[0]) if n == 5 else (1, 0)
+    return _KV.pack(_p(k), _p(v), _dt(k), layers, lst, st[-4], st[-3], st[-2], pages, page, H, D, _p(page_table),
+                    max(tst[0], entries), entries), H, D, R
 
 
-def _node_rows(t, dtype=None):
+def _node_rows(t, shape, dtype):
     """Row stride of [R, T, heads, head_dim] whose heads lie side by side, the rows of all requests at one stride."""
-    R, T, H, D = t.shape
-    st = t.stride()
-    if (D > 1 and st[3] != 1) or (H > 1 and st[2] != D) or (R > 1 and T > 1 and st[0] != T * st[1]):
-        raise ValueError("expected [R, T, heads, head_dim] with heads side by side and one row stride")
-    if dtype is not None and t.dtype != dtype:
+    if t.shape != shape:
+        raise ValueError(f"expected the shape {tuple(shape)}, got {tuple(t.shape)}: the tensors do not fit together")
+    if t.dtype is not dtype:
         raise TypeError(f"expected {dtype}, got {t.dtype}")
-    return st[1] if T > 1 else st[0] if R > 1 else H * D
+    R, T, H, D = shape
+    s0, s1, s2, s3 = t.stride()
+    if (s3 != 1 and D > 1) or (s2 != D and H > 1) or (s0 != T * s1 and R > 1 and T > 1):
+        raise ValueError("expected [R, T, heads, head_dim] with heads side by side and one row stride")
+    return s1 if T > 1 else s0 if R > 1 else H * D
 
 
 def _i32(t, *shape):
     """Pointer of a contiguous int32 device tensor of this shape (None: no tensor)."""
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"expected a contiguous int32 tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
     return _p(t)
 
@@ -477,25 +489,22 @@ def dspark_rope_append(q, k, v, pos, cos_sin, k_cache, v_cache, page_table, ctx_
     """Turns q [R, T, Hq, D] and k [R, T, H, D] by their positions pos [R, T] or [R, T, axes] (table cos_sin
     [P, rot] float32, axis [rot / 2] int32) and writes k and v to the nodes' slots of the paged cache.
     Returns (q_out, status); out may be q itself."""
-    R, T, Hq, D = q.shape
-    c = _kvcache(k_cache, v_cache, page_table)
-    H = c.heads
-    if k.shape != (R, T, H, D) or v.shape != k.shape or D != c.head_dim or page_table.shape[0] != R:
-        raise ValueError("q, k, v, the cache and its page table do not fit together")
-    out = torch.empty((R, T, Hq, D), dtype=q.dtype, device=q.device) if out is None else out
-    if out.shape != q.shape:
-        raise ValueError("out has another shape than q")
+    qs = q.shape
+    R, T, Hq, D = qs
+    c, H, Dc, Rt = _kvcache(k_cache, v_cache, page_table)
+    if D != Dc or Rt != R:
+        raise ValueError("q, the cache and its page table do not fit together")
+    dt, ks = k_cache.dtype, (R, T, H, D)
+    out = torch.empty(qs, dtype=dt, device=q.device) if out is None else out
     status = new_status(q.device) if status is None else status
-    A = 1 if pos.dim() == 2 else pos.shape[2]
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+    A = pos.shape[2] if pos.dim() == 3 else 1
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
         raise ValueError("expected a contiguous float32 table cos_sin [P, rot]")
     P, rot = cos_sin.shape
-    _check(lib().dspark_rope_append(_p(q), _node_rows(q, k_cache.dtype), _p(k), _node_rows(k, k_cache.dtype), _p(v),
-                                    _node_rows(v, k_cache.dtype), R, T, Hq,
-                                    _i32(pos, R, T) if pos.dim() == 2 else _i32(pos, R, T, A), A, _p(cos_sin), P, rot,
-                                    _i32(axis, rot // 2), int(interleaved), ctypes.byref(c), _i32(ctx_len, R),
-                                    _i32(n_nodes, R), _p(out), _node_rows(out, k_cache.dtype), _p(status),
-                                    _stream(stream)), "dspark_rope_append")
+    _check(lib().dspark_rope_append(_p(q), _node_rows(q, qs, dt), _p(k), _node_rows(k, ks, dt), _p(v), _node_rows(v, ks, dt), R, T,
+                                    Hq, _i32(pos, R, T, A) if pos.dim() == 3 else _i32(pos, R, T), A, _p(cos_sin), P, rot,
+                                    _i32(axis, rot // 2), int(interleaved), c, _i32(ctx_len, R), _i32(n_nodes, R), _p(out),
+                                    _node_rows(out, qs, dt), _p(status), _stream(stream)), "dspark_rope_append")
     return out, status
 
 
@@ -504,27 +513,24 @@ def dspark_tree_attention(q, k_cache, v_cache, page_table, ctx_len, *, mask=None
     """Attention of the nodes' queries q [R, T, Hq, D] over the committed slots and the nodes that mask
     [R, T, W] shows (None: chains). lse: None (allocated), a float32 [R, T, Hq] tensor, or False (not
     written). Returns (out, lse, status)."""
-    R, T, Hq, D = q.shape
-    c = _kvcache(k_cache, v_cache, page_table)
-    if D != c.head_dim or page_table.shape[0] != R:
+    qs = q.shape
+    R, T, Hq, D = qs
+    c, H, Dc, Rt = _kvcache(k_cache, v_cache, page_table)
+    if D != Dc or Rt != R:
         raise ValueError("q, the cache and its page table do not fit together")
-    dev = q.device
-    out = torch.empty((R, T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
-    if out.shape != q.shape:
-        raise ValueError("out has another shape than q")
+    dt = k_cache.dtype
+    out = torch.empty(qs, dtype=dt, device=q.device) if out is None else out
     if lse is None:
-        lse = torch.empty((R, T, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty((R, T, Hq), dtype=torch.float32, device=q.device)
     elif lse is False:
         lse = None
-    elif lse.shape != (R, T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    elif lse.shape != (R, T, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous():
         raise ValueError("expected a contiguous float32 lse [R, T, Hq]")
-    status = new_status(dev) if status is None else status
-    ws = workspace(OP_TREE_ATTENTION, R, T, Hq * D, c.heads, dev) if ws is None else ws
-    wp, wn = _ws(ws)
-    scale = D ** -0.5 if scale is None else scale
-    _check(lib().dspark_tree_attention(_p(q), _node_rows(q, k_cache.dtype), R, T, Hq, ctypes.byref(c), _i32(ctx_len, R),
-                                       _i32(n_nodes, R), _i32(mask, R, T, (T + 31) // 32), scale, softcap, _p(out),
-                                       _node_rows(out, k_cache.dtype), _p(lse), wp, wn, _p(status), _stream(stream)),
+    status = new_status(q.device) if status is None else status
+    wp, wn = _ws(workspace(OP_TREE_ATTENTION, R, T, Hq * D, H, q.device) if ws is None else ws)
+    _check(lib().dspark_tree_attention(_p(q), _node_rows(q, qs, dt), R, T, Hq, c, _i32(ctx_len, R), _i32(n_nodes, R),
+                                       _i32(mask, R, T, (T + 31) // 32), D ** -0.5 if scale is None else scale, softcap,
+                                       _p(out), _node_rows(out, qs, dt), _p(lse), wp, wn, _p(status), _stream(stream)),
            "dspark_tree_attention")
     return out, lse, status
 
@@ -548,12 +554,11 @@ def dspark_cache_commit(k_cache, v_cache, page_table, ctx_len, path, n_accepted,
     """Moves the accepted nodes' rows (path [R, T], n_accepted [R] int32) to the front of their requests'
     drafted slots, in every layer of k_cache / v_cache ([layers, pages, page, heads, head_dim] or one
     layer). path None: chains of T nodes, only the length changes. Returns (new_len [R], status)."""
-    c = _kvcache(k_cache, v_cache, page_table)
-    R = page_table.shape[0]
+    c, _, _, R = _kvcache(k_cache, v_cache, page_table)
     if path is not None:
         T = path.shape[1]
     out = torch.empty((R,), dtype=torch.int32, device=ctx_len.device) if out is None else out
     status = new_status(ctx_len.device) if status is None else status
-    _check(lib().dspark_cache_commit(ctypes.byref(c), _i32(ctx_len, R), _i32(path, R, T), _i32(n_accepted, R), R, T,
+    _check(lib().dspark_cache_commit(c, _i32(ctx_len, R), _i32(path, R, T), _i32(n_accepted, R), R, T,
                                      _i32(out, R), _p(status), _stream(stream)), "dspark_cache_commit")
     return out, status

@@ -924,6 +924,8 @@ extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64
   CUtensorMap mk, mv;
   const bool maps = tc && ta_tensor_map(&mk, cache->k, *cache, box) && ta_tensor_map(&mv, cache->v, *cache, box);
   a.kt = maps ? TA_KT : 64;
+  // the running tile count of all requests is 32 bits wide (lengths are cut to what the table holds)
+  DS_REQUIRE(R * ds_ceil_div(std::min<int64_t>(int64_t(cache->table_pages) * cache->page_size, int64_t(INT32_MAX)) + TA_MAXT, a.kt) <= INT32_MAX);
   a.box = box;
   if (maps) {
     a.rpg = a.rows > 128 ? 256 : 128;

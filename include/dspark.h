@@ -475,8 +475,8 @@ dspark_status dspark_rope_append(const void* q, int64_t ldq, const void* k, int6
  * no effect on it, infinities and NaN included. Sums and statistics are float32; with bf16 the
  * products run on the tensor cores and the weights p are rounded to bf16 for the product with v
  * (bf16 caches with head_dim <= 128, page_size % 8 == 0 and 16-byte aligned rows; others in float32).
- * scale > 0, softcap >= 0 finite. R <= 1024, T 1..512, Hq <= 1024. The result does not depend on
- * the run: no atomics. ws: dspark_workspace_size(DSPARK_OP_TREE_ATTENTION, R, T, Hq * head_dim,
+ * scale > 0, softcap >= 0 finite. R <= 1024, T 1..512, Hq <= 1024, R * table_pages * page_size <
+ * 2^37. The result does not depend on the run: no atomics. ws: dspark_workspace_size(DSPARK_OP_TREE_ATTENTION, R, T, Hq * head_dim,
  * heads) bytes.
  */
 dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64_t R, int32_t T, int32_t Hq,
