@@ -21,19 +21,18 @@ constexpr int TF_KEYS = 64;
 constexpr int TF_THREADS = 256;
 constexpr int TF_LDP = TF_KEYS + 4;
 
-// Shared memory: 8 RW query rows as float32; the key tile, whose place the weights take; the value tile.
+// Shared memory: 8 RW query rows as float32, four columns of all rows side by side, so that a warp's rows lie at
+// constant offsets; the key tile, whose place the weights take; the value tile, its rows a constant 32 UC apart.
 template <typename T>
 struct TfLayout {
-  int ldq, ldk, ldv;           // elements of a row
+  int ldk;                     // elements of a key row
   size_t q, k, v;              // bytes of each
-  __host__ __device__ TfLayout(int D, int rows) {
-    ldq = D + 4;
+  __host__ __device__ TfLayout(int D, int rows, int uc) {
     ldk = D + 16 / int(sizeof(T));
-    ldv = D;
-    q = size_t(rows) * ldq * 4;
+    q = size_t(rows) * D * 4;
     const size_t kb = size_t(TF_KEYS) * ldk * sizeof(T), pb = size_t(rows) * TF_LDP * 4;
     k = kb > pb ? kb : pb;
-    v = size_t(TF_KEYS) * ldv * sizeof(T);
+    v = size_t(TF_KEYS) * uc * 32 * sizeof(T);
   }
   __host__ __device__ size_t total() const { return q + k + v; }
 };
@@ -78,9 +77,10 @@ __global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const Ta
   __shared__ TaLens s_len;
   __shared__ int64_t s_at[TF_KEYS];
   const int D = a.c.head_dim, tid = threadIdx.x, lane = tid & 31, row0 = (tid >> 5) * RW;
-  const TfLayout<T> lay(D, RW * 8);
+  constexpr int ROWS = RW * 8, LDV = UC * 32;
+  const TfLayout<T> lay(D, ROWS, UC);
   uint8_t* base = reinterpret_cast<uint8_t*>(smem4);
-  float* sQ = reinterpret_cast<float*>(base);
+  float4* sQ = reinterpret_cast<float4*>(base);       // [D / 4][ROWS]
   T* sK = reinterpret_cast<T*>(base + lay.q);
   float* sP = reinterpret_cast<float*>(base + lay.q);
   T* sV = reinterpret_cast<T*>(base + lay.q + lay.k);
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const Ta
           x = vecq ? tf_4(at)
                    : make_float4(ds_load_elem<T>(at), ds_load_elem<T>(at + 1), ds_load_elem<T>(at + 2), ds_load_elem<T>(at + 3));
         }
-        if (tid < per * step) *reinterpret_cast<float4*>(sQ + lr * lay.ldq + c * 4) = x;
+        if (tid < per * step) sQ[c * ROWS + lr] = x;
         for (h += step; h >= a.G; h -= a.G) ++i;
       }
     }
@@ -133,17 +133,20 @@ __global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const Ta
       if (tid < TF_KEYS) s_at[tid] = mine;
       __syncthreads();                               // also: the tile before is used up
       tf_copy(sK, lay.ldk, kc, s_at, D, veckv);
-      tf_copy(sV, lay.ldv, vc, s_at, D, veckv);
+      tf_copy(sV, LDV, vc, s_at, D, veckv);
       mine = tid < TF_KEYS ? slot_of(t + 1) : -1;
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();
       float s[RW][2] = {};
+      const float4* qp = sQ + row0;
+      const T* kp = sK + lane * lay.ldk;
+      const T* kq = kp + 32 * lay.ldk;
 #pragma unroll 1
-      for (int d = 0; d < D; d += 4) {
-        const float4 k0 = tf_4(sK + lane * lay.ldk + d), k1 = tf_4(sK + (lane + 32) * lay.ldk + d);
+      for (int d = 0; d < D; d += 4, qp += ROWS, kp += 4, kq += 4) {
+        const float4 k0 = tf_4(kp), k1 = tf_4(kq);
 #pragma unroll
         for (int x = 0; x < RW; ++x) {
-          const float4 qx = tf_4(sQ + (row0 + x) * lay.ldq + d);
+          const float4 qx = qp[x];
           s[x][0] = __fmaf_rn(qx.x, k0.x, s[x][0]);
           s[x][1] = __fmaf_rn(qx.x, k1.x, s[x][1]);
           s[x][0] = __fmaf_rn(qx.y, k0.y, s[x][0]);
@@ -184,7 +187,8 @@ __global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const Ta
       // that holds nodes, every weight is looked at; else an unseen key's weight counts as 0.
       bool odd = false;
       if (masked) {
-        for (int u = tid; u < TF_KEYS * (D / 4); u += TF_THREADS) {      // the rows lie one after the other
+        for (int u = tid; u < TF_KEYS * (LDV / 4); u += TF_THREADS) {
+          if (u % (LDV / 4) * 4 >= D) continue;      // columns past head_dim hold anything
           const float4 y = tf_4(sV + u * 4);
           odd = odd || !(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY);
         }
@@ -193,12 +197,14 @@ __global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const Ta
       const int keys = int(min(int64_t(TF_KEYS), (len - key0 + 3) & ~int64_t(3)));   // past them all weights are -1
       auto add = [&](auto mode) {                    // 0: all seen, 1: unseen keys among them, 2: odd values too
         constexpr int MODE = decltype(mode)::value;
+        const float* wp = sP + row0 * TF_LDP;
+        const T* vp = sV + lane;
 #pragma unroll 1
-        for (int j = 0; j < keys; j += 4) {
+        for (int j = 0; j < keys; j += 4, wp += 4, vp += 4 * LDV) {
           float w[RW][4];
 #pragma unroll
           for (int x = 0; x < RW; ++x) {
-            const float4 y = tf_4(sP + (row0 + x) * TF_LDP + j);
+            const float4 y = tf_4(wp + x * TF_LDP);
             w[x][0] = y.x; w[x][1] = y.y; w[x][2] = y.z; w[x][3] = y.w;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const Ta
           for (int e = 0; e < 4; ++e) {
 #pragma unroll
             for (int u = 0; u < UC; ++u) {
-              const float y = ds_load_elem<T>(sV + (j + e) * lay.ldv + min(lane + 32 * u, D - 1));
+              const float y = ds_load_elem<T>(vp + e * LDV + 32 * u);
 #pragma unroll
               for (int x = 0; x < RW; ++x) {
                 if (MODE == 2 && w[x][e] < 0.0f) continue;
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const Ta
 
 template <typename T, int RW, int UC>
 cudaError_t tf_launch(const TaArgs& a, int grid, cudaStream_t st) {
-  const size_t smem = TfLayout<T>(a.c.head_dim, RW * 8).total();
+  const size_t smem = TfLayout<T>(a.c.head_dim, RW * 8, UC).total();
   const cudaError_t e = ds_ensure_smem(reinterpret_cast<const void*>(tree_attn_float_kernel<T, RW, UC>), smem);
   if (e != cudaSuccess) return e;
   return ds_launch(tree_attn_float_kernel<T, RW, UC>, dim3(unsigned(grid)), dim3(TF_THREADS), smem, st, a,
