@@ -468,9 +468,19 @@ def _i32(t, *shape):
     return _p(t)
 
 
+def _on(stream, fn, given):
+    """fn with the arguments it was given, on `stream`: what it allocates (outputs, a status word, a workspace)
+    is then made, cleared and later reused in that stream's order."""
+    given = dict(given, stream=None)
+    with torch.cuda.stream(stream):
+        return fn(**given)
+
+
 def dspark_tree_mask(parent, *, R=None, T=None, n_nodes=None, base=None, out=None, status=None, stream=None, device="cuda"):
     """Ancestor mask and positions of drafted trees: parent [R, T] int32 (None: chains of R x T) ->
     (mask [R, T, W] int32 words, pos [R, T] int32, status)."""
+    if stream is not None:
+        return _on(stream, dspark_tree_mask, locals())
     if parent is not None:
         R, T = parent.shape
         device = parent.device
@@ -489,6 +499,8 @@ def dspark_rope_append(q, k, v, pos, cos_sin, k_cache, v_cache, page_table, ctx_
     """Turns q [R, T, Hq, D] and k [R, T, H, D] by their positions pos [R, T] or [R, T, axes] (table cos_sin
     [P, rot] float32, axis [rot / 2] int32) and writes k and v to the nodes' slots of the paged cache.
     Returns (q_out, status); out may be q itself."""
+    if stream is not None:
+        return _on(stream, dspark_rope_append, locals())
     qs = q.shape
     R, T, Hq, D = qs
     c, H, Dc, Rt = _kvcache(k_cache, v_cache, page_table)
@@ -513,6 +525,8 @@ def dspark_tree_attention(q, k_cache, v_cache, page_table, ctx_len, *, mask=None
     """Attention of the nodes' queries q [R, T, Hq, D] over the committed slots and the nodes that mask
     [R, T, W] shows (None: chains). lse: None (allocated), a float32 [R, T, Hq] tensor, or False (not
     written). Returns (out, lse, status)."""
+    if stream is not None:
+        return _on(stream, dspark_tree_attention, locals())
     qs = q.shape
     R, T, Hq, D = qs
     c, H, Dc, Rt = _kvcache(k_cache, v_cache, page_table)
@@ -538,6 +552,8 @@ def dspark_tree_attention(q, k_cache, v_cache, page_table, ctx_len, *, mask=None
 def dspark_tree_accept(tokens, parent, best, *, n_nodes=None, out=None, status=None, stream=None):
     """Greedy acceptance along a tree: node tokens, parents (None: chains) and the target's choice after each
     node, all [R, T] int32 -> (out_tokens [R, T], n_accepted [R], path [R, T], status)."""
+    if stream is not None:
+        return _on(stream, dspark_tree_accept, locals())
     R, T = tokens.shape
     dev = tokens.device
     if out is None:
@@ -554,6 +570,8 @@ def dspark_cache_commit(k_cache, v_cache, page_table, ctx_len, path, n_accepted,
     """Moves the accepted nodes' rows (path [R, T], n_accepted [R] int32) to the front of their requests'
     drafted slots, in every layer of k_cache / v_cache ([layers, pages, page, heads, head_dim] or one
     layer). path None: chains of T nodes, only the length changes. Returns (new_len [R], status)."""
+    if stream is not None:
+        return _on(stream, dspark_cache_commit, locals())
     c, _, _, R = _kvcache(k_cache, v_cache, page_table)
     if path is not None:
         T = path.shape[1]

@@ -221,6 +221,25 @@ def test_same_bits_every_time_on_any_stream_and_in_a_graph():
     assert not torch.equal(out2, first) and int(st) == 0
 
 
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """With the current stream busy, calls on another stream neither wait for it nor use memory it still works on."""
+    import dspark_draft_selection_gb300 as ds
+    c = Case(10, 12, 8, 2, 64, 16, [200, 33], None).run()
+    want, want_lse = c.out.clone(), c.lse.clone()
+    ctx, n = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (c.ctx, c.n))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    got = [ds.dspark_tree_attention(c.q, c.k, c.v, c.table, ctx, mask=c.mask, n_nodes=n, scale=c.scale, stream=side) for _ in range(4)]
+    mask, pos, st = ds.dspark_tree_mask(None, R=2, T=70, stream=side)
+    with torch.cuda.stream(side):
+        for out, lse, status in got:
+            assert torch.equal(out, want) and torch.equal(lse, want_lse) and int(status) == 0
+        assert int(st) == 0 and torch.equal(pos[0], torch.arange(70, device="cuda", dtype=torch.int32))
+    assert not torch.cuda.current_stream().query()           # the current stream was still at it
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_pages_past_two_to_the_31_elements(dtype):
     import dspark_draft_selection_gb300 as ds
