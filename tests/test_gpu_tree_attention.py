@@ -228,14 +228,21 @@ def test_what_a_call_allocates_belongs_to_its_stream():
     want, want_lse = c.out.clone(), c.lse.clone()
     ctx, n = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (c.ctx, c.n))
     side = torch.cuda.Stream()
+    places = torch.arange(70, device="cuda", dtype=torch.int32)
+
+    def on_side():
+        got = [ds.dspark_tree_attention(c.q, c.k, c.v, c.table, ctx, mask=c.mask, n_nodes=n, scale=c.scale, stream=side) for _ in range(4)]
+        mask, pos, st = ds.dspark_tree_mask(None, R=2, T=70, stream=side)
+        with torch.cuda.stream(side):
+            for out, lse, status in got:
+                assert torch.equal(out, want) and torch.equal(lse, want_lse) and int(status) == 0
+            assert int(st) == 0 and torch.equal(pos[0], places)
+
+    torch.cuda.synchronize()
+    on_side()                                                # the stream's memory is there: no call below has to allocate
     torch.cuda.synchronize()
     torch.cuda._sleep(400_000_000)
-    got = [ds.dspark_tree_attention(c.q, c.k, c.v, c.table, ctx, mask=c.mask, n_nodes=n, scale=c.scale, stream=side) for _ in range(4)]
-    mask, pos, st = ds.dspark_tree_mask(None, R=2, T=70, stream=side)
-    with torch.cuda.stream(side):
-        for out, lse, status in got:
-            assert torch.equal(out, want) and torch.equal(lse, want_lse) and int(status) == 0
-        assert int(st) == 0 and torch.equal(pos[0], torch.arange(70, device="cuda", dtype=torch.int32))
+    on_side()
     assert not torch.cuda.current_stream().query()           # the current stream was still at it
     torch.cuda.synchronize()
 
