@@ -21,10 +21,10 @@
 // Bound: HBM (2 D bytes of keys and of values per cached token and key head) up to about 128 query rows per
 // key head, above that the chain P V, Q K^T, softmax of a group: S and P share their tensor memory (S, O of
 // both groups take all 512 columns), so a group's next scores wait for its P V. Measured with the join:
-//   32 requests of 8 nodes x 4 heads, 300-8,200 keys   110 us   5.2 TB/s, 0.76 of the measured copy rate
-//   64 requests of one token x 4 heads, 300-8,200 keys 188 us   6.0 TB/s, 0.89
-//   4 trees of 64 nodes x 8 heads, 40,000-65,600 keys  193 us   982 TFLOP/s; with a cap 254 us, 748 TFLOP/s
-//   one token x 4 heads, 4,097 keys                     15 us   two tiles a block: latency
+//   32 requests of 8 nodes x 4 heads, 300-8,200 keys   112 us   5.1 TB/s, 0.75 of the measured copy rate
+//   64 requests of one token x 4 heads, 300-8,200 keys 189 us   6.0 TB/s, 0.88
+//   4 trees of 64 nodes x 8 heads, 40,000-65,600 keys  193 us   982 TFLOP/s; with a cap 260 us, 730 TFLOP/s
+//   one token x 4 heads, 4,097 keys                     16 us   two tiles a block: latency
 #include "tree_attn.cuh"
 
 extern "C" size_t dspark_internal_ws_tree_attention(int64_t R, int32_t T, int64_t cols, int32_t heads);
@@ -36,7 +36,7 @@ constexpr int TA_THREADS = 384;
 constexpr int TA_QTHREADS = 32;
 constexpr uint32_t TA_CHUNK = 128 * 128;   // bytes of 128 rows x 64 bf16 columns
 constexpr float TA_RISE = 8.0f;            // rise of the maximum (log2) that rescales O
-constexpr float TA_FIXED = 80.0f;          // caps (log2) up to which the reference stays 0
+constexpr float TA_FIXED = 80.0f;          // caps (log2) up to which a reference may serve for good
 
 template <int DP, bool TWO>
 __host__ __device__ constexpr int ta_stages() {
@@ -204,7 +204,7 @@ __device__ __noinline__ void ta_row_again(const TaArgs& a, int r, int32_t ctx, i
     s = ds_warp_sumf(s);
     const float x = a.softcap > 0.0f ? ta_tanh(s * (a.scale * 2.0f * TA_LOG2E / a.softcap), a.softcap * TA_LOG2E)
                                      : s * (a.scale * TA_LOG2E);
-    const float p = ta_ex2(x - mref);
+    const float p = __bfloat162float(__float2bfloat16_rn(ta_ex2(x - mref)));   // as the sums of rounded weights expect
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int d = d0 + lane + 32 * u;
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
   __shared__ uint32_t s_tmem, s_seq[NS];               // s_seq: sequence number + 1 of a stage's last copy
   __shared__ int s_abort;
   __shared__ TaLens s_len;
-  __shared__ float2 s_ml[2][2][128];                   // [piece parity][group][row]
+  __shared__ float4 s_ml[2][2][128];                   // [piece parity][group][row]
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     const uint32_t tS = tl + TS + 128 * g, tO = tl + TO + DP * g;
     const float sc = CAP ? a.scale * 2.0f * TA_LOG2E / a.softcap : a.scale * TA_LOG2E;
     const float cap2 = a.softcap * TA_LOG2E, sy = CAP ? a.scale / a.softcap : 0.0f;
-    const bool fixed = CAP && cap2 <= TA_FIXED;                // the reference stays 0
+    const bool fixed = CAP && cap2 <= TA_FIXED;                // references may serve for good
     const int D = a.c.head_dim;
     uint32_t np = 0, ns = 0, seq = 0;
     bool first = true, ok = true;
@@ -477,7 +477,10 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
       const int m = p.g * a.rpg + (TWO ? g * 128 : 0) + lr;    // this thread's row
       const bool live = p.g * a.rpg + (TWO ? g * 128 : 0) + quarter * 32 < a.rows;   // any row of this warp
       const int i = min(m, a.rows - 1) / a.G;
-      float mref = fixed ? 0.0f : -INFINITY, l = 0.0f;         // reference (log2) and sum of this thread's row
+      // reference (log2), sum of the weights and, with one row tile, of the weights rounded to bf16: the result
+      // is divided by the latter, so that a row whose weight lies on few keys keeps its accuracy (one key: v
+      // itself). Two row tiles (many rows) take the first sum for both: there the softmax bounds the kernel.
+      float mref = -INFINITY, l = 0.0f, lr16 = 0.0f;
       bool has = false;                                        // O holds an earlier tile
       for (int t = TWO ? 0 : g; t < npt; t += TWO ? 1 : 2) {
         ok = wait(&s_sfull[g], ns++, first ? a.first_wait : DS_WAIT_LIMIT);
@@ -521,6 +524,10 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
             }
             ta_tmem_wait_st();
           }
+          // Under a cap up to TA_FIXED (log2) a reference of at least -TA_FIXED / 4 serves for good: what follows is at
+          // most 2^100 times as large, which weights, their sums and O hold (2^17 keys x the values), so the tile
+          // needs no maximum.
+          const bool skip = CAP && fixed && __all_sync(0xFFFFFFFFu, mref >= -0.25f * TA_FIXED);
           // chains of four maxima, and below of four sums, side by side: one would wait for itself
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mg4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           {
@@ -530,7 +537,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) mg4[(e >> 1) & 3] = fmaxf(mg4[(e >> 1) & 3], fmaxf(fabsf(v[e]), fabsf(v[e + 1])));
               }
-              if (CAP && fixed) return;
+              if (CAP && skip) return;
               if (CAP && masked) {
                 const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 32 * c);
 #pragma unroll
@@ -555,8 +562,6 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           const float mg = fmaxf(fmaxf(mg4[0], mg4[1]), fmaxf(mg4[2], mg4[3]));
           float v[16];
           ta_tmem_fetch(tS, v);
-          // Under a cap the exponents stay within +-cap log2(e); up to TA_FIXED that fits the range of the
-          // weights, their sums and O (2^80 x 2^17 keys x the values), so no maximum is needed.
           const float m2 = mx == -INFINITY ? -INFINITY : CAP ? ta_tanh(mx * sc, cap2) : mx * sc;
           const bool up = m2 > mref + TA_RISE || (mref == -INFINITY && m2 > -INFINITY);
           if (__any_sync(0xFFFFFFFFu, up)) {
@@ -573,6 +578,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
               }
             }
             l *= f;
+            lr16 *= f;
             if (up) mref = m2;
           }
           const float mu = mref == -INFINITY ? 0.0f : mref;
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           // the polynomials where every score of the warp is well below the cap, else the exponential form
           const bool narrow = CAP && __all_sync(0xFFFFFFFFu, mg * sy <= 0.375f);
           const bool wide = CAP && __all_sync(0xFFFFFFFFu, mg * sy <= 1.0f);
-          uint64_t sum[4] = {0, 0, 0, 0};
+          uint64_t sum[4] = {0, 0, 0, 0}, sum16[2] = {0, 0};
           auto put = [&](const uint64_t (&x)[8], int c) {      // weights of 16 keys: exponentials, sums, P
             uint32_t w[8];
 #pragma unroll
@@ -588,6 +594,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
               const float x0 = ta_ex2(ds_f2lo(x[e])), x1 = ta_ex2(ds_f2hi(x[e]));
               sum[e & 3] = ds_add2(sum[e & 3], ds_f2(x0, x1));
               w[e] = ta_pack(x0, x1);
+              if (!TWO) sum16[e & 1] = ds_add2(sum16[e & 1], ds_f2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)));
             }
             ta_tmem_st_x8(tS + 8 * c, w);
           };
@@ -643,6 +650,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           }
           sum[0] = ds_add2(ds_add2(sum[0], sum[1]), ds_add2(sum[2], sum[3]));
           l += ds_f2lo(sum[0]) + ds_f2hi(sum[0]);
+          sum16[0] = ds_add2(sum16[0], sum16[1]);
+          if (!TWO) lr16 += ds_f2lo(sum16[0]) + ds_f2hi(sum16[0]);
           ta_tmem_wait_st();
         }
         has = true;
@@ -653,7 +662,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
       if (!ok) break;
       // ---- the piece's result ----
       if (!TWO) {
-        s_ml[np & 1][g][lr] = make_float2(mref, l);
+        s_ml[np & 1][g][lr] = make_float4(mref, l, lr16, 0.0f);
         __syncwarp();
         if (lane == 0) ds_mbar_arrive(&s_mlfull);
       }
@@ -665,14 +674,17 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
         const bool valid = m < a.rows && i < n;
         float w0 = 1.0f, w1 = 0.0f;
         if (!TWO) {
-          const float2 x = s_ml[np & 1][0][lr], y = s_ml[np & 1][1][lr];
+          const float4 x = s_ml[np & 1][0][lr], y = s_ml[np & 1][1][lr];
           mref = fmaxf(x.x, y.x);
           w0 = x.x == -INFINITY ? 0.0f : ta_ex2(x.x - mref);
           w1 = y.x == -INFINITY ? 0.0f : ta_ex2(y.x - mref);
           l = w0 * x.y + w1 * y.y;
+          lr16 = w0 * x.z + w1 * y.z;
+        } else {
+          lr16 = l;
         }
         const bool any = valid && l != 0.0f;                   // also when l is not a number
-        const float inv = any ? 1.0f / l : 0.0f;
+        const float inv = any ? 1.0f / lr16 : 0.0f;
         const bool whole = p.whole();
         const int d0 = TWO ? 0 : g * (DP / 2), d1 = TWO ? DP : d0 + DP / 2;
         const int64_t slot = p.slot(blockIdx.x);
@@ -721,7 +733,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
         }
         __syncwarp();
         if (m < a.rows && (TWO || g == 0)) {
-          if (!whole) a.part_ml[slot * a.rs + m - p.g * a.rpg] = valid ? make_float2(mref, l) : make_float2(-INFINITY, 0.0f);
+          if (!whole) a.part_ml[slot * a.rs + m - p.g * a.rpg] = valid ? make_float4(mref, l, lr16, 0.0f) : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
           else if (a.lse) a.lse[row * a.Hq + h] = any ? (mref + log2f(l)) * TA_LN2 : -INFINITY;
         }
         // rows that came out not finite with nodes among the keys
@@ -780,7 +792,7 @@ __global__ void __launch_bounds__(256) tree_attn_join_kernel(const TaArgs a, uin
   const int b0 = holder(g0);
   if (start(b0 + 1) >= g0 + nt) return;                // whole
   const int np = holder(g0 + nt - 1) - b0 + 1;
-  float M = -INFINITY, L = 0.0f;
+  float M = -INFINITY, L = 0.0f, Ld = 0.0f;            // Ld: the sum that the result is divided by
   float4 o[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -789,12 +801,13 @@ __global__ void __launch_bounds__(256) tree_attn_join_kernel(const TaArgs a, uin
     const int64_t s0 = start(b0 + k0 + lane), s1 = start(b0 + k0 + lane + 1);
     const bool there = k0 + lane < np && s1 > s0;
     const int32_t slot = 2 * (b0 + k0 + lane) + (s0 > g0 ? 0 : 1);
-    const float2 ml = there ? __ldcg(a.part_ml + int64_t(slot) * a.rs + lrow) : make_float2(-INFINITY, 0.0f);
+    const float4 ml = there ? __ldcg(a.part_ml + int64_t(slot) * a.rs + lrow) : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
     const float before = M;
     M = fmaxf(M, ds_warp_max(ml.x));
     const bool seen = ml.y != 0.0f;                    // also a sum that is not a number
     const float w = seen ? ta_ex2(ml.x - M) : 0.0f, f = before == -INFINITY ? 0.0f : ta_ex2(before - M);
     L = __fmaf_rn(w, ml.y, L * f);
+    Ld = __fmaf_rn(w, ml.z, Ld * f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       o[u].x *= f;
@@ -831,8 +844,9 @@ __global__ void __launch_bounds__(256) tree_attn_join_kernel(const TaArgs a, uin
     }
   }
   L = ds_warp_sumf(L);
+  Ld = ds_warp_sumf(Ld);
   const bool any = L != 0.0f;
-  const float inv = any ? 1.0f / L : 0.0f;
+  const float inv = any ? 1.0f / Ld : 0.0f;
   T* out = reinterpret_cast<T*>(a.out) + row * a.ldo + int64_t(h) * D;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -890,14 +904,14 @@ constexpr size_t TA_WS_PREF = 4352;        // pref[TA_MAXR + 1], rounded up to 2
 
 }  // namespace
 
-// Partial results of 2 slots per block: rs rows x (head_dim sums + maximum and sum). rs * head_dim is at
+// Partial results of 2 slots per block: rs rows x (head_dim sums + reference and sums). rs * head_dim is at
 // most the group's T * cols / heads, and at most 256 rows of 256 columns (one block per SM) or 64 rows of
-// 256 (the float32 kernel's two blocks); head_dim >= 8, so the two statistics add at most a quarter.
+// 256 (the float32 kernel's two blocks); head_dim >= 8, so a row's statistics (16 bytes) add at most a half.
 extern "C" size_t dspark_internal_ws_tree_attention(int64_t R, int32_t T, int64_t cols, int32_t heads) {
   if (R <= 0 || T <= 0 || cols <= 0 || heads <= 0) return 0;
   const int64_t item = int64_t(T) * (cols / heads), sms = ds_num_sms();
   const int64_t vals = std::max(2 * sms * std::min<int64_t>(item, 256 * 256), 4 * sms * std::min<int64_t>(item, 64 * 256));
-  return TA_WS_PREF + size_t(ds_ceil_div(vals * 5, 256) * 256);
+  return TA_WS_PREF + size_t(ds_ceil_div(vals * 6, 256) * 256);
 }
 
 extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64_t R, int32_t T, int32_t Hq,
@@ -951,7 +965,7 @@ extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   a.pref = reinterpret_cast<int32_t*>(w);
   a.part_o = reinterpret_cast<float*>(w + TA_WS_PREF);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * a.rs * D);
+  a.part_ml = reinterpret_cast<float4*>(a.part_o + slots * a.rs * D);
   // 64 columns have their own form: 64 rows 52.6 us, 512 rows 165 us, padded to 128 columns 57.8 and 178 us.
   if (maps) DS_CUDA_TRY(D <= 64 ? ta_dispatch_tc<64>(a, grid, mk, mv, stream) : ta_dispatch_tc<128>(a, grid, mk, mv, stream));
   else DS_CUDA_TRY(ta_launch_float(a, grid, stream));

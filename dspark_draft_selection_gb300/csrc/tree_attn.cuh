@@ -26,7 +26,7 @@ struct TaArgs {
   float scale, softcap;
   float2 wide[7], narrow[4];   // coefficients of the cap's polynomials, each twice
   int32_t* pref;               // [R + 1] running sum of the requests' tile counts
-  float2* part_ml;             // [slots][rs] (reference maximum in log2 units, sum)
+  float4* part_ml;             // [slots][rs] (reference in log2 units, sum of the weights, sum the result is divided by)
   float* part_o;               // [slots][rs][D] sums of weights times values, relative to the maximum
   int32_t* status;
   uint32_t first_wait;

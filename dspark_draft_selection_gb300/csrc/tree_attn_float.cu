@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(TF_THREADS, 2) tree_attn_float_kernel(const Ta
       const int64_t row = int64_t(p.r) * a.T + i;
       const float inv = any ? 1.0f / l[x] : 0.0f;
       if (lane == 0) {
-        if (!whole) a.part_ml[slot * a.rs + lr] = valid ? make_float2(mref[x], l[x]) : make_float2(-INFINITY, 0.0f);
+        if (!whole) a.part_ml[slot * a.rs + lr] = valid ? make_float4(mref[x], l[x], l[x], 0.0f) : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
         else if (a.lse) a.lse[row * a.Hq + h] = any ? (mref[x] + log2f(l[x])) * TA_LN2 : -INFINITY;
       }
 #pragma unroll

@@ -123,6 +123,21 @@ def test_long_ragged_contexts_are_split_and_joined(dtype, T, Hq):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("softcap", [0.0, 30.0, 200.0])
+@pytest.mark.parametrize("T", [1, 3, 90])                    # one tile of rows, two
+def test_one_key_gives_its_value(dtype, softcap, T):
+    """Nothing committed and nodes that see themselves alone: the weight is 1, so the result is v, whatever the score."""
+    c = Case(T, T, 4, 2, 64, 16, [0, 0], None, dtype, mask="block", scale=2.0, softcap=softcap)
+    c.sees = np.broadcast_to(np.eye(T, dtype=bool), (2, T, T))
+    c.mask = dev(np.ascontiguousarray(tree.words(c.sees)))
+    c.run()
+    assert int(c.status) == 0
+    for r in range(2):
+        v = slots_of(c.v, c.table, r, T)
+        assert torch.equal(c.out[r], v.repeat_interleave(2, 1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_maxima_that_keep_rising(dtype):
     """Keys that grow along the cache move the running maximum at every tile; the mean of v keeps its accuracy."""
     c = Case(5, 4, 4, 2, 64, 32, [1500], None, dtype, mask="chain")
