@@ -331,13 +331,6 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
       }
       base += 2 * npt;
     }
-    // After a wait that ran out, the copies in flight land before the block leaves (otherwise the MMA warp
-    // has waited for every one of them).
-    for (int k = 0; k < NS && aborted(); ++k) {
-      const uint32_t v = *reinterpret_cast<volatile uint32_t*>(&s_seq[k]);
-      if (v) (void)ds_mbar_wait(&s_full[k], ((v - 1) / NS) & 1u, DS_WAIT_LIMIT);
-    }
-    __syncwarp();
   } else if (warp == 1) {
     // ---- one lane issues the MMAs. QK of a group's next tile follows the group's PV: S and P share
     // tensor memory, and the MMAs of one thread run in order ----
@@ -759,7 +752,14 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     }
   }
   __syncthreads();
+  // After a wait that ran out, the copies in flight land before the block leaves its shared memory to another
+  // (otherwise the MMA warp has waited for every one of them). Only here, past the barrier, has every copy been
+  // issued and does every warp know of the wait.
   if (warp == 1) {
+    if (aborted())
+      for (int k = 0; k < NS; ++k)
+        if (s_seq[k]) (void)ds_mbar_wait(&s_full[k], ((s_seq[k] - 1) / NS) & 1u, DS_WAIT_LIMIT);
+    __syncwarp();
     ds_tc_fence_after();
     ds_tmem_dealloc(tmem, 512);
   }
