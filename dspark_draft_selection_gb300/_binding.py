@@ -440,10 +440,13 @@ def _kvcache(k, v, page_table):
     if len(tsh) != 2 or tst[1] != 1 or page_table.dtype is not _I32:
         raise ValueError("expected an int32 page table [R, pages] with unit column stride")
     R, entries = tsh
+    ld = tst[0] if R > 1 else entries                      # a single row's stride says nothing
+    if ld < entries:                                       # an expanded table: row r would be read past its end
+        raise ValueError("the page table's rows overlap: make it contiguous, or give every request its own row")
     pages, page, H, D = sh[-4:]
     layers, lst = (sh[0], st[0]) if n == 5 else (1, 0)
     return _KV.pack(_p(k), _p(v), _dt(k), layers, lst, st[-4], st[-3], st[-2], pages, page, H, D, _p(page_table),
-                    max(tst[0], entries), entries), H, D, R
+                    ld, entries), H, D, R
 
 
 def _node_rows(t, shape, dtype):
