@@ -181,42 +181,56 @@ DS_DEV uint32_t ta_pack(float lo, float hi) {
   return r;
 }
 
-// The row again in plain float32, every key looked at by itself: used for a row whose result came out
-// not finite where drafted nodes are among the keys. The product P V adds 0 * v for a node that the
-// row does not see, and that is not a number when v is not finite; here such a node is passed over.
-// One warp per row; writes columns [d0, d1) relative to the reference maximum `mref`, times `mul`.
-__device__ __noinline__ void ta_row_again(const TaArgs& a, int r, int32_t ctx, int32_t n, int hk, int m, int64_t k0,
-                                          int64_t k1, float mref, float mul, int d0, int d1, __nv_bfloat16* out,
-                                          float* part) {
-  const int lane = threadIdx.x & 31;
-  const int i = m / a.G, h = hk * a.G + m % a.G, D = a.c.head_dim;
-  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t(r) * a.T + i) * a.ldq + int64_t(h) * D;
-  const __nv_bfloat16* kc = reinterpret_cast<const __nv_bfloat16*>(a.c.k) + hk * a.c.head_stride;
-  const __nv_bfloat16* vc = reinterpret_cast<const __nv_bfloat16*>(a.c.v) + hk * a.c.head_stride;
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  k1 = min(k1, int64_t(ctx) + n);
-  for (int64_t j = k0; j < k1; ++j) {
-    if (!(ta_mask32(a, r, i, n, j - ctx) & 1u)) continue;
-    const int64_t at = ta_slot(a, r, j);
-    float s = 0.0f;
-    if (at >= 0)
-      for (int d = lane; d < D; d += 32) s = __fmaf_rn(__bfloat162float(q[d]), __bfloat162float(kc[at + d]), s);
-    s = ds_warp_sumf(s);
-    const float x = a.softcap > 0.0f ? ta_tanh(s * (a.scale * 2.0f * TA_LOG2E / a.softcap), a.softcap * TA_LOG2E)
-                                     : s * (a.scale * TA_LOG2E);
-    const float p = __bfloat162float(__float2bfloat16_rn(ta_ex2(x - mref)));   // as the sums of rounded weights expect
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int d = d0 + lane + 32 * u;
-      if (d < d1) acc[u] = __fmaf_rn(p, at >= 0 ? __bfloat162float(vc[at + d]) : 0.0f, acc[u]);
+// Bit 15 and bit 31 are set where the two bf16 numbers of x are infinite or not a number.
+DS_DEV uint32_t ta_odd(uint32_t x) { return ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// A value tile with nodes or with the end of the keys, before P multiplies it: 0 times a value that is not finite is
+// not 0, and neither need be 0 times what follows the last key in its page. Rows [k0, k1) of the tile, past the last
+// key, become 0; rows [f, k0) are nodes, the first of them `node`, whose values that are not finite become 0 too and
+// whose bits in `odd` are set before: ta_add_odd gives them to the rows that see such a node. One group's threads;
+// two groups on one tile both do this, and each finds what was there or what the other left, which ends the same.
+// (Out of line, like ta_add_odd: the code of a tile stays short.)
+template <int NC>
+__device__ __noinline__ void ta_clean(uint8_t* st, int f, int k0, int k1, int node, uint32_t* odd, int thread) {
+  for (int u = thread; u < (k1 - f) * NC * 8; u += 128) {
+    const int key = u / (NC * 8), c = u % (NC * 8);
+    uint4* at = reinterpret_cast<uint4*>(st + (c >> 3) * TA_CHUNK + (f + key) * 128 + ((c & 7) << 4));
+    if (f + key >= k0) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
     }
+    const uint4 y = *at;
+    if ((ta_odd(y.x) | ta_odd(y.y) | ta_odd(y.z) | ta_odd(y.w)) == 0u) continue;
+    atomicOr(odd + ((node + key) >> 5), 1u << ((node + key) & 31));
+    __threadfence_block();
+    auto finite = [](uint32_t x) { return x & ~((ta_odd(x) >> 15) * 0xFFFFu); };
+    *at = make_uint4(finite(y.x), finite(y.y), finite(y.z), finite(y.w));
   }
+}
+
+// What nodes whose values are not finite add to a row that sees them: a weight is more than 0, so its product with an
+// infinity or with what is not a number is that value itself. One thread a row; `out` (the result) or `part` (a
+// partial one) holds the row without them, this thread having written columns [d0, d1).
+__device__ __noinline__ void ta_add_odd(const TaArgs& a, int r, int32_t ctx, int32_t n, int i, int hk, int d0, int d1,
+                                        const uint32_t* odd, __nv_bfloat16* out, float* part) {
+  const __nv_bfloat16* vc = reinterpret_cast<const __nv_bfloat16*>(a.c.v) + hk * a.c.head_stride;
+  for (int w = 0; w < a.W; ++w) {
+    if (odd[w] == 0u) continue;
+    for (uint32_t bits = odd[w] & ta_mask32(a, r, i, n, 32 * w); bits; bits &= bits - 1) {
+      const int64_t at = ta_slot(a, r, int64_t(ctx) + 32 * w + __ffs(int(bits)) - 1);
+      if (at < 0) continue;
+      for (int d = d0; d < d1; d += 8) {
+        const uint4 y = *reinterpret_cast<const uint4*>(vc + at + d);
+        const uint32_t x[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int d = d0 + lane + 32 * u;
-    if (d >= d1) continue;
-    if (out) out[d] = __float2bfloat16_rn(acc[u] * mul);
-    else part[d] = acc[u];
+        for (int e = 0; e < 8; ++e) {
+          if (!(ta_odd(x[e >> 1]) & (e & 1 ? 0x80000000u : 0x8000u))) continue;
+          const float z = __uint_as_float(e & 1 ? x[e >> 1] & 0xFFFF0000u : x[e >> 1] << 16);
+          if (out) out[d + e] = __float2bfloat16_rn(__bfloat162float(out[d + e]) + z);
+          else part[d + e] += z;
+        }
+      }
+    }
   }
 }
 
@@ -234,6 +248,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
   __shared__ int s_abort;
   __shared__ TaLens s_len;
   __shared__ float4 s_ml[2][2][128];                   // [piece parity][group][row]
+  __shared__ uint4 s_odd[3][TA_MAXT / 128];            // [piece modulo 3]: a bit for every node with a value that is not finite
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -244,6 +259,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tmK) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tmV) : "memory");
   }
+  if (tid < 3 * (TA_MAXT / 128)) s_odd[tid / (TA_MAXT / 128)][tid % (TA_MAXT / 128)] = make_uint4(0, 0, 0, 0);
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       ds_mbar_init(&s_full[s], 1);
@@ -475,6 +491,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
       // itself). Two row tiles (many rows) take the first sum for both: there the softmax bounds the kernel.
       float mref = -INFINITY, l = 0.0f, lr16 = 0.0f;
       bool has = false;                                        // O holds an earlier tile
+      const int tn = ctx / TA_KT - p.t0;                       // tiles from here on hold nodes or the end of the keys
       for (int t = TWO ? 0 : g; t < npt; t += TWO ? 1 : 2) {
         ok = wait(&s_sfull[g], ns++, first ? a.first_wait : DS_WAIT_LIMIT);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -482,26 +499,12 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
         if (!ok) break;
         ds_tc_fence_after();
         const int64_t key0 = int64_t(p.t0 + t) * TA_KT;
-        if (key0 + TA_KT > len) {
-          // the item's last tile: values past the last key may be anything in the page, and 0 times
-          // that need not be 0
-          const uint32_t sv = seq + (TWO ? 2 * t + 1 : min(npt, t + 2) + t);
-          ok = __all_sync(0xFFFFFFFFu, wait(&s_full[sv % NS], sv / NS, DS_WAIT_LIMIT));
-          if (!ok) break;
-          const int k0 = int(len - key0), k1 = min(TA_KT, (k0 + a.box - 1) / a.box * a.box);
-          uint8_t* st = sR + (sv % NS) * STAGE;
-          for (int u = lr; u < (k1 - k0) * NC * 8; u += 128) {
-            const int key = k0 + u / (NC * 8), c = u % (NC * 8);
-            *reinterpret_cast<uint4*>(st + (c >> 3) * TA_CHUNK + key * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
-          }
-          ds_fence_proxy_async_smem();
-        }
         if (live) {
           // Masks matter only in tiles that hold nodes or the end of the keys. Without a cap they are put
           // into S beforehand; with one they are looked up after it, and the longer code stays in loops (as
           // straight lines it waits for instructions more than it saves).
           constexpr int FLAT = CAP ? 1 : 8;
-          const bool masked = key0 + TA_KT > ctx;
+          const bool masked = t >= tn;
           const int64_t nd = key0 - ctx;
           if (!CAP && masked) {
 #pragma unroll 1
@@ -647,6 +650,15 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           if (!TWO) lr16 += ds_f2lo(sum16[0]) + ds_f2hi(sum16[0]);
           ta_tmem_wait_st();
         }
+        if (t >= tn) {
+          const uint32_t sv = seq + (TWO ? 2 * t + 1 : min(npt, t + 2) + t);
+          ok = __all_sync(0xFFFFFFFFu, wait(&s_full[sv % NS], sv / NS, DS_WAIT_LIMIT));
+          if (!ok) break;
+          const int f = int(max(int64_t(ctx) - key0, int64_t(0))), k0 = int(min(len - key0, int64_t(TA_KT)));
+          ta_clean<NC>(sR + (sv % NS) * STAGE, f, k0, min(TA_KT, (k0 + a.box - 1) / a.box * a.box), int(key0 + f - ctx),
+                       reinterpret_cast<uint32_t*>(s_odd[np % 3]), lr);
+          ds_fence_proxy_async_smem();
+        }
         has = true;
         ds_tc_fence_before();
         __syncwarp();
@@ -685,7 +697,6 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
         const int64_t row = int64_t(p.r) * a.T + i;
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + row * a.ldo + int64_t(h) * D;
         float* part = a.part_o + (slot * a.rs + (m - p.g * a.rpg)) * D;
-        float chk = 0.0f;
 #pragma unroll 1
         for (int c = 0; c < (TWO ? DP : DP / 2) / 16; ++c) {
           const int d = d0 + 16 * c;
@@ -705,8 +716,6 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
             }
           }
           if (d < D && m < a.rows) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) chk = __fmaf_rn(o[e], 0.0f, chk);
             if (whole) {
 #pragma unroll
               for (int e = 0; e < 16; e += 8) {
@@ -729,21 +738,17 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           if (!whole) a.part_ml[slot * a.rs + m - p.g * a.rpg] = valid ? make_float4(mref, l, lr16, 0.0f) : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
           else if (a.lse) a.lse[row * a.Hq + h] = any ? (mref + log2f(l)) * TA_LN2 : -INFINITY;
         }
-        // rows that came out not finite with nodes among the keys
-        uint32_t redo = __ballot_sync(0xFFFFFFFFu, any && !(chk == 0.0f) && int64_t(p.t1) * TA_KT > ctx);
-        while (redo) {
-          const int src = __ffs(int(redo)) - 1;
-          redo &= redo - 1;
-          const int mm = __shfl_sync(0xFFFFFFFFu, m, src);
-          const float mr = __shfl_sync(0xFFFFFFFFu, mref, src), iv = __shfl_sync(0xFFFFFFFFu, inv, src);
-          const int ii = mm / a.G;
-          ta_row_again(a, p.r, ctx, n, p.hk, mm, int64_t(p.t0) * TA_KT, int64_t(p.t1) * TA_KT, mr, iv, d0, min(d1, D),
-                       whole ? reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t(p.r) * a.T + ii) * a.ldo +
-                                   int64_t(p.hk * a.G + mm - ii * a.G) * D
-                             : nullptr,
-                       a.part_o + (slot * a.rs + (mm - p.g * a.rpg)) * D);
+        if (int64_t(p.t1) * TA_KT > ctx) {
+          const uint32_t* odd = reinterpret_cast<const uint32_t*>(s_odd[np % 3]);
+          uint32_t marks = 0;
+#pragma unroll 1
+          for (int w = 0; w < a.W; ++w) marks |= odd[w];
+          if (marks && valid) ta_add_odd(a, p.r, ctx, n, i, p.hk, d0, min(d1, D), odd, whole ? out : nullptr, part);
         }
       }
+      // Marks of this piece's nodes. (Those of the piece before are no longer read: O was free for this piece after
+      // every warp was done with that one. They are cleared for the piece after the next.)
+      if (warp == 4 && lane < TA_MAXT / 128) s_odd[(np + 2) % 3][lane] = make_uint4(0, 0, 0, 0);
       ds_tc_fence_before();
       __syncwarp();
       if (lane == 0) ds_mbar_arrive(&s_ofree);

@@ -1,10 +1,44 @@
-"""Edges of dspark_tree_attention."""
+"""Edges of dspark_tree_attention. Tolerances as in test_gpu_tree_attention.py; a cap's own
+error is 2^-20 of the smaller of the cap and the scores' magnitude (a score's rounding is relative to itself)."""
+import numpy as np
 import pytest
 import torch
 
+from oracle import tree
+from tests.test_gpu_cache import f64, slots_of
 from tests.test_gpu_tree_attention import Case
 
 pytestmark = pytest.mark.gpu
+
+
+def place(c, r, j):
+    """Index of slot j of request r in the cache."""
+    return int(c.table[r, j // c.page]), j % c.page
+
+
+def against_oracle(c, requests, rows=None):
+    """Every element of the result, infinities with their sign and what is not a number included."""
+    assert int(c.status) == 0
+    for r in requests:
+        ctx, n = c.ctx[r], c.n[r]
+        i = np.arange(c.T) if rows is None else np.array(rows)
+        sees = np.concatenate([np.ones((c.T, ctx), bool), c.sees[r][:, :n]], 1)
+        sees[n:] = False
+        k, v = (f64(slots_of(x, c.table, r, ctx + n)) for x in (c.k, c.v))
+        with np.errstate(invalid="ignore"):
+            want, lse, mag, big = tree.attention(f64(c.q[r])[i], k, v, sees[i], c.scale, c.softcap)
+        eps = 2 * (c.D + 8) * 2.0 ** -24 * big + 2.0 ** -20 + (ctx + n) * 2.0 ** -24 + 2.0 ** -20 * np.minimum(c.softcap, big)
+        half = 2.0 ** -8 * (1 + 2.0 ** -7) if c.dtype == "bf16" else 0.0
+        got, got_lse = f64(c.out[r])[i], f64(c.lse[r])[i]
+        fin = np.isfinite(want)
+        np.testing.assert_array_equal(got[~fin], want[~fin])
+        with np.errstate(invalid="ignore"):
+            tol, off = (eps[..., None] + half) * mag + half * np.abs(want) + 1e-30, np.abs(got - want)
+        bad = ~(off[fin] <= tol[fin])
+        assert not bad.any(), (r, int(bad.sum()), (off[fin] / tol[fin]).max())
+        ok = np.isfinite(lse)
+        np.testing.assert_array_equal(got_lse[~ok], lse[~ok])
+        assert np.all(np.abs(got_lse[ok] - lse[ok]) <= (eps + 2.0 ** -22 * (1 + np.abs(lse)))[ok])
 
 
 # --- a wait that ran out ---
@@ -28,3 +62,111 @@ def test_a_wait_that_ran_out_leaves_nothing_in_flight(R, ctx, T):
         _, lse, _ = ds.dspark_tree_attention(c.q, c.k, c.v, c.table, lens, scale=c.scale, out=out, ws=ws, status=good)
         assert int(late) == 6 and int(good) == 0
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+# --- values that are not finite ---
+SIZES = [(8, 8), (40, 16)]                                   # T, query heads on two key heads: one tile of rows, two
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,Hq", SIZES)
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_nodes_with_values_that_are_not_finite_behind_thousands_of_keys(dtype, T, Hq, softcap):
+    """Rows that see such a node get what the sum gives in its columns, the others and the other columns are as
+    without it: several nodes, both infinities in one column, one node in the last place."""
+    c = Case(T, T, Hq, 2, 128, 16, [3001, 130], [T, T - 1], dtype, softcap=softcap)
+    for r in range(2):
+        last = c.n[r] - 1
+        for j, h, col, x in ((1, 0, 5, float("inf")), (2, 0, 5, -float("inf")), (2, 1, 77, float("nan")), (4, 1, 0, float("inf")),
+                             (last, 0, 127, -float("inf")), (last, 1, 64, float("nan"))):
+            c.v[place(c, r, c.ctx[r] + j)][h, col] = x
+    rows = None if T < 10 else [0, 1, 2, 3, 4, 5, 17, T - 2, T - 1]
+    c.run()
+    against_oracle(c, (0, 1), rows)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,Hq", SIZES)
+def test_committed_values_that_are_not_finite_reach_every_row(dtype, T, Hq):
+    c = Case(T, T, Hq, 2, 64, 16, [1030, 20], None, dtype)
+    for j, h, col, x in ((3, 0, 9, float("inf")), (1029, 1, 8, float("nan")), (1028, 0, 8, -float("inf"))):
+        c.v[place(c, 0, j)][h, col] = x
+    c.v[place(c, 0, 1030 + 2)][0, 9] = -float("inf")         # and a node against the committed infinity
+    c.run()
+    against_oracle(c, (0, 1), None if T < 10 else [0, 1, 2, 3, 9, T - 1])
+
+
+def test_every_node_with_values_that_are_not_finite():
+    """The widest tree, every value of it: rows whose mask holds nothing keep their committed mean."""
+    c = Case(7, 512, 2, 1, 64, 16, [700], None, mask="any")
+    for j in range(512):
+        c.v[place(c, 0, 700 + j)] = float("nan") if j % 2 else float("inf")
+    c.run()
+    against_oracle(c, (0,), [0, 1, 2, 3, 4, 250, 252, 510, 511])
+
+
+@pytest.mark.parametrize("T,Hq", [(8, 8), (64, 8)])
+@pytest.mark.parametrize("where", ["committed", "node"])
+def test_a_value_that_is_not_finite_takes_no_longer(T, Hq, where):
+    """One bad value in one request of many, whose items have one block each: the call's time is a clean call's
+    (three times as much at most, for the clocks' sake)."""
+    import dspark_draft_selection_gb300 as ds
+    R = 80
+    c = Case(3, T, Hq, 2, 64, 16, [2000] * R, None, mask="chain")
+    ctx = torch.tensor(c.ctx, dtype=torch.int32, device="cuda")
+    ws, st, out = ds.workspace(ds.OP_TREE_ATTENTION, R, T, Hq * 64, 2), ds.new_status(), torch.empty_like(c.q)
+
+    def took():
+        best = 1e9
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            a.record()
+            ds.dspark_tree_attention(c.q, c.k, c.v, c.table, ctx, out=out, ws=ws, status=st)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    clean = took()
+    good = out.clone()
+    c.v[place(c, 41, 700 if where == "committed" else 2001)] = float("nan")
+    got = took()
+    assert int(st) == 0 and torch.isnan(out[41].float()).any() and torch.equal(out[:41], good[:41]) and torch.equal(out[42:], good[42:])
+    assert got < 3 * clean, (got, clean)
+
+
+# --- what is not seen ---
+def same_bits_whatever_is_not_seen(dtype, softcap, T, Hq):
+    """Keys past the end, keys of nodes that a row does not see and other rows' queries: ordinary ones, large ones or
+    nothing sensible, the row's bits are the same."""
+    c = Case(12, T, Hq, 2, 64, 16, [333, 20], [T, T - 3], dtype, softcap=softcap)
+    c.run()
+    assert int(c.status) == 0
+    out, lse = c.out.clone(), c.lse.clone()
+    used = torch.zeros(c.k.shape[:2], dtype=torch.bool, device="cuda")
+    for r in range(2):
+        for j in range(c.ctx[r] + c.n[r]):
+            used[place(c, r, j)] = True
+    for junk in (0.0, 60.0, 3e38, float("inf"), float("nan")):
+        c.k[~used], c.v[~used] = junk, junk
+        c.run()
+        assert int(c.status) == 0 and torch.equal(c.out, out) and torch.equal(c.lse, lse), junk
+    node = 2
+    blind = [i for i in range(T) if not c.sees[0, i, node]]
+    assert blind and not c.sees[0, blind[-1], node]
+    at = place(c, 0, c.ctx[0] + node)
+    keep = c.k[at].clone(), c.v[at].clone(), c.q[0, node].clone()
+    for junk in (0.0, 60.0, 3e38, float("inf"), float("nan")):
+        c.k[at], c.v[at], c.q[0, node] = junk, junk, junk
+        c.run()
+        assert int(c.status) == 0, junk
+        assert torch.equal(c.out[0, blind], out[0, blind]) and torch.equal(c.lse[0, blind], lse[0, blind]), junk
+        assert torch.equal(c.out[1], out[1])
+    c.k[at], c.v[at], c.q[0, node] = keep
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,Hq", [(9, 4), (70, 4)])
+def test_what_is_not_seen_changes_no_bit(dtype, T, Hq):
+    same_bits_whatever_is_not_seen(dtype, 0.0, T, Hq)
