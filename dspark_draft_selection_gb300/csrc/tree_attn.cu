@@ -12,9 +12,10 @@
 //   O[128 rows, D] += P V                  (A from tensor memory, V as it lies: D-major)
 // Two softmax groups of four warps alternate so that the tensor pipe works on one while the other
 // computes weights: with more than 128 rows they hold different rows of the same key tile, else the
-// even and the odd key tiles of the same rows, joined through tensor memory at the end. O is rescaled
-// only when a row's maximum rises by more than 8 in log2 (the weights stay below 256; sums are relative
-// to the same reference, so the result is the same softmax).
+// even and the odd key tiles of the same rows, joined through tensor memory at the end. The reference m lies
+// 8 (in log2) above the maximum that set it, and O is rescaled only when a score passes it: no weight is above
+// 1, so no sum is larger than the largest value times the keys, whatever the scores and the cap. (Sums are
+// relative to the same reference, so the result is the same softmax; float32 and bf16 hold weights down to 2^-126.)
 //
 // Roles: warps 0 and 2 copy key and value tiles with TMA, one box per page piece, into a ring of stages;
 // warp 1 issues the MMAs; warp 3 copies the query rows; warps 4-7 and 8-11 are the softmax groups.
@@ -35,8 +36,7 @@ constexpr int TA_KT = 128;                 // keys per tile
 constexpr int TA_THREADS = 384;
 constexpr int TA_QTHREADS = 32;
 constexpr uint32_t TA_CHUNK = 128 * 128;   // bytes of 128 rows x 64 bf16 columns
-constexpr float TA_RISE = 8.0f;            // rise of the maximum (log2) that rescales O
-constexpr float TA_FIXED = 80.0f;          // caps (log2) up to which a reference may serve for good
+constexpr float TA_ABOVE = 8.0f;           // a new reference lies this far (log2) above the maximum
 
 template <int DP, bool TWO>
 __host__ __device__ constexpr int ta_stages() {
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     const uint32_t tS = tl + TS + 128 * g, tO = tl + TO + DP * g;
     const float sc = CAP ? a.scale * 2.0f * TA_LOG2E / a.softcap : a.scale * TA_LOG2E;
     const float cap2 = a.softcap * TA_LOG2E, sy = CAP ? a.scale / a.softcap : 0.0f;
-    const bool fixed = CAP && cap2 <= TA_FIXED;                // references may serve for good
+    const float lin = a.scale * TA_LOG2E;                      // |capped score| <= min(cap, |score|)
     const int D = a.c.head_dim;
     uint32_t np = 0, ns = 0, seq = 0;
     bool first = true, ok = true;
@@ -520,20 +520,21 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
             }
             ta_tmem_wait_st();
           }
-          // Under a cap up to TA_FIXED (log2) a reference of at least -TA_FIXED / 4 serves for good: what follows is at
-          // most 2^100 times as large, which weights, their sums and O hold (2^17 keys x the values), so the tile
-          // needs no maximum.
-          const bool skip = CAP && fixed && __all_sync(0xFFFFFFFFu, mref >= -0.25f * TA_FIXED);
-          // chains of four maxima, and below of four sums, side by side: one would wait for itself
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mg4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          {
+          // Under a cap the largest |score| is looked for first, which picks the cap's form below. No row's maximum is
+          // above it (and its linear bound), so tiles in which that is below every row's reference need no maximum.
+          bool maxima = !CAP || masked || __any_sync(0xFFFFFFFFu, mref == -INFINITY);
+          float mx = -INFINITY, mg = 0.0f;
+#pragma unroll 1
+          for (;;) {
+            // chains of four maxima, and below of four sums, side by side: one would wait for itself
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mg4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             float va[32], vb[32];
             auto look = [&](float (&v)[32], int c) {
               if (CAP) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) mg4[(e >> 1) & 3] = fmaxf(mg4[(e >> 1) & 3], fmaxf(fabsf(v[e]), fabsf(v[e + 1])));
               }
-              if (CAP && skip) return;
+              if (CAP && !maxima) return;
               if (CAP && masked) {
                 const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 32 * c);
 #pragma unroll
@@ -553,15 +554,18 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
               if (c == 0) ta_tmem_fetch(tS + 64, va);
               look(vb, c + 1);
             }
+            mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            mg = fmaxf(fmaxf(mg4[0], mg4[1]), fmaxf(mg4[2], mg4[3]));
+            if (maxima || !__any_sync(0xFFFFFFFFu, fminf(cap2, mg * lin) > mref)) break;
+            maxima = true;
           }
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          const float mg = fmaxf(fmaxf(mg4[0], mg4[1]), fmaxf(mg4[2], mg4[3]));
           float v[16];
           ta_tmem_fetch(tS, v);
           const float m2 = mx == -INFINITY ? -INFINITY : CAP ? ta_tanh(mx * sc, cap2) : mx * sc;
-          const bool up = m2 > mref + TA_RISE || (mref == -INFINITY && m2 > -INFINITY);
+          // (the bound again, so that a row does the same whoever made its warp look for maxima)
+          const bool up = m2 > mref && (!CAP || fminf(cap2, mg * lin) > mref);
           if (__any_sync(0xFFFFFFFFu, up)) {
-            const float f = up ? ta_ex2(mref - m2) : 1.0f;     // 0 from -inf
+            const float to = m2 + TA_ABOVE, f = up ? ta_ex2(mref - to) : 1.0f;     // 0 from -inf
             if (has) {
 #pragma unroll 1
               for (int c = 0; c < DP / 16; ++c) {
@@ -575,7 +579,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
             }
             l *= f;
             lr16 *= f;
-            if (up) mref = m2;
+            if (up) mref = to;
           }
           const float mu = mref == -INFINITY ? 0.0f : mref;
           const uint64_t nm2 = ds_f2(-mu, -mu);

@@ -472,7 +472,8 @@ dspark_status dspark_rope_append(const void* q, int64_t ldq, const void* k, int6
  *   x = scale q . k; softcap > 0: x = softcap tanh(x / softcap); p = softmax of x over what i sees;
  *   out = sum p v; lse (nullable) [R, T, Hq] float32 = log of the sum of exp x.
  * A row that sees nothing, and slots i >= n_r, give zeros and lse = -inf. What a row does not see has
- * no effect on it, infinities and NaN included. Sums and statistics are float32; with bf16 the
+ * no effect on it, infinities and NaN included. Sums and statistics are float32, of weights of at most 1:
+ * a result is finite where a row's |v|, summed over the keys it sees, stays below 2^128. With bf16 the
  * products run on the tensor cores and the weights p are rounded to bf16 for the product with v
  * (bf16 caches with head_dim <= 128, page_size % 8 == 0 and 16-byte aligned rows; others in float32).
  * scale > 0, softcap >= 0 finite. R <= 1024, T 1..512, Hq <= 1024, R * table_pages * page_size <

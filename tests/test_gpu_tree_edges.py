@@ -170,3 +170,52 @@ def same_bits_whatever_is_not_seen(dtype, softcap, T, Hq):
 @pytest.mark.parametrize("T,Hq", [(9, 4), (70, 4)])
 def test_what_is_not_seen_changes_no_bit(dtype, T, Hq):
     same_bits_whatever_is_not_seen(dtype, 0.0, T, Hq)
+
+
+# --- the range of values ---
+def along(c, r, h, scores):
+    """Keys of request r, key head h, whose scores with every query (all of them made alike) are as given."""
+    D = c.D
+    unit = torch.ones(D, device="cuda")
+    unit[::3] = -1.0
+    c.q[r] = unit.to(c.q.dtype)
+    s = torch.arange(len(scores), device="cuda")
+    at = c.table[r].long()[s // c.page], s % c.page
+    k = torch.tensor(scores, dtype=torch.float64, device="cuda")[:, None] / (D * c.scale) * unit
+    c.k[at[0], at[1], h] = k.to(c.k.dtype)
+    return at
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [2, 70])                       # one tile of rows, two
+@pytest.mark.parametrize("softcap", [20.0, 38.0, 50.0, 55.0])
+def test_scores_that_reach_the_cap_late_with_large_values(dtype, T, softcap):
+    """Hundreds of keys a little below zero, then some at the cap, in items that one block holds whole: whatever the reference
+    was, finite values stay finite."""
+    R = 90
+    c = Case(5, T, 4, 2, 64, 16, [900] * R, None, dtype, mask="chain", scale=0.125, softcap=softcap)
+    scores = np.full(900, -12.0)
+    scores[[300, 301, 700, 899]] = 3000.0
+    for r in (0, 8, 89):
+        for h in range(2):
+            along(c, r, h, scores)
+    c.v *= 2.0 ** 60
+    c.run()
+    against_oracle(c, (0, 8, 89), None if T < 10 else [0, 1, 35, T - 1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [2, 70])
+@pytest.mark.parametrize("softcap", [0.0, 50.0])
+def test_rows_that_see_a_value_near_the_types_largest(dtype, T, softcap):
+    """Maxima that rise by a few units behind the first tiles of items that one block holds whole, and a value of 3e38 on a
+    key at the top."""
+    R = 90
+    c = Case(6, T, 4, 2, 64, 16, [500] * R, None, dtype, mask="chain", scale=0.125, softcap=softcap)
+    scores = np.concatenate([np.linspace(-2, 0, 256), np.linspace(0, 4.5, 244)])
+    for r in (0, 7, 89):
+        for h in range(2):
+            at = along(c, r, h, scores)
+            c.v[int(at[0][497]), int(at[1][497]), h, 3:7] = 3e38
+    c.run()
+    against_oracle(c, (0, 7, 89), None if T < 10 else [0, 1, 35, T - 1])
