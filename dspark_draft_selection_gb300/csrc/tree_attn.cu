@@ -561,7 +561,9 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           }
           float v[16];
           ta_tmem_fetch(tS, v);
-          const float m2 = mx == -INFINITY ? -INFINITY : CAP ? ta_tanh(mx * sc, cap2) : mx * sc;
+          // (under a cap the form that serves its score: the exponential one loses scores far below the cap)
+          const float m2 = mx == -INFINITY ? -INFINITY : !CAP ? mx * sc : fabsf(mx) * sy <= 1.0f ? mx * ds_f2lo(ta_poly_wide(a, ds_f2(mx, mx)))
+                                                                                               : ta_tanh(mx * sc, cap2);
           // (the bound again, so that a row does the same whoever made its warp look for maxima)
           const bool up = m2 > mref && (!CAP || fminf(cap2, mg * lin) > mref);
           if (__any_sync(0xFFFFFFFFu, up)) {

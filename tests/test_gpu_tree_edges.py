@@ -219,3 +219,13 @@ def test_rows_that_see_a_value_near_the_types_largest(dtype, T, softcap):
             c.v[int(at[0][497]), int(at[1][497]), h, 3:7] = 3e38
     c.run()
     against_oracle(c, (0, 7, 89), None if T < 10 else [0, 1, 35, T - 1])
+
+
+# --- caps far from the scores ---
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [5, 70])
+@pytest.mark.parametrize("softcap", [1e-3, 0.3, 1e3, 1e5, 1e7, 1e10, 1e20, 3e38])
+def test_caps_far_from_the_scores(dtype, T, softcap):
+    """A cap far above the scores is no cap; one far below them leaves the signs."""
+    c = Case(11, T, 4, 2, 64, 16, [600, 31], None, dtype, softcap=softcap).run()
+    against_oracle(c, (0, 1), None if T < 10 else [0, 1, 35, T - 1])
