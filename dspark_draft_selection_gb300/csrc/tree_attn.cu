@@ -135,14 +135,14 @@ DS_DEV void ta_arrived(float (&v)[16]) {
 // cap2 * tanh(sy * s) = s * Q(s^2): tanh(y) = y P(y^2) with the coefficients of P that make the largest
 // relative error smallest (fitted by reweighted least squares), scaled by the powers of sy and by cap2; two
 // values at a time. Seven coefficients serve |y| <= 1 and four |y| <= 0.375; as evaluated in float32 their
-// errors are 1.6e-7 and 1.5e-7. The scaled coefficients are kernel arguments (a pair of each), made by
-// ta_tanh_coefficients.
+// errors are 1.6e-7 and 1.5e-7. The scaled coefficients are kernel arguments, made by ta_tanh_coefficients (the narrow
+// ones a pair of each).
 DS_DEV uint64_t ta_pair(float2 x) { return ds_f2(x.x, x.y); }
-DS_DEV uint64_t ta_poly_wide(const TaArgs& a, uint64_t s) {
+DS_DEV uint64_t ta_poly(const float (&co)[7], uint64_t s) {   // a row's own: the wide ones, or the narrow ones and zeros
   const uint64_t u = ds_fma2(s, s, 0);
-  uint64_t q = ta_pair(a.wide[6]);
+  uint64_t q = ds_f2(co[6], co[6]);
 #pragma unroll
-  for (int k = 5; k >= 0; --k) q = ds_fma2(q, u, ta_pair(a.wide[k]));
+  for (int k = 5; k >= 0; --k) q = ds_fma2(q, u, ds_f2(co[k], co[k]));
   return q;
 }
 DS_DEV uint64_t ta_poly_narrow(const TaArgs& a, uint64_t s) {
@@ -500,13 +500,13 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
         ds_tc_fence_after();
         const int64_t key0 = int64_t(p.t0 + t) * TA_KT;
         if (live) {
-          // Masks matter only in tiles that hold nodes or the end of the keys. Without a cap they are put
-          // into S beforehand; with one they are looked up after it, and the longer code stays in loops (as
-          // straight lines it waits for instructions more than it saves).
+          // Masks matter only in tiles that hold nodes or the end of the keys. They are put into S beforehand: -inf, or,
+          // under a cap, what is not a number, which neither maximum takes up (there they are looked up again after
+          // the cap, and the longer code stays in loops: as straight lines it waits for instructions more than it saves).
           constexpr int FLAT = CAP ? 1 : 8;
           const bool masked = t >= tn;
           const int64_t nd = key0 - ctx;
-          if (!CAP && masked) {
+          if (masked) {
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
               float v[16];
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
               const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 16 * c);
               __syncwarp();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = (bits >> e) & 1u ? __float_as_uint(v[e]) : 0xFF800000u;
+              for (int e = 0; e < 16; ++e) w[e] = (bits >> e) & 1u ? __float_as_uint(v[e]) : CAP ? 0x7FFFFFFFu : 0xFF800000u;
               ta_tmem_st_x16(tS + 16 * c, w);
             }
             ta_tmem_wait_st();
@@ -533,13 +533,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
               if (CAP) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) mg4[(e >> 1) & 3] = fmaxf(mg4[(e >> 1) & 3], fmaxf(fabsf(v[e]), fabsf(v[e + 1])));
-              }
-              if (CAP && !maxima) return;
-              if (CAP && masked) {
-                const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 32 * c);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = (bits >> e) & 1u ? v[e] : -INFINITY;
-                __syncwarp();
+                if (!maxima) return;
               }
 #pragma unroll
               for (int e = 0; e < 32; e += 2) mx4[(e >> 1) & 3] = fmaxf(mx4[(e >> 1) & 3], fmaxf(v[e], v[e + 1]));
@@ -561,11 +555,21 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           }
           float v[16];
           ta_tmem_fetch(tS, v);
-          // (under a cap the form that serves its score: the exponential one loses scores far below the cap)
-          const float m2 = mx == -INFINITY ? -INFINITY : !CAP ? mx * sc : fabsf(mx) * sy <= 1.0f ? mx * ds_f2lo(ta_poly_wide(a, ds_f2(mx, mx)))
-                                                                                               : ta_tanh(mx * sc, cap2);
+          // A row's form of the cap goes by the scores that it sees, so that its result is the same whatever the others
+          // are; the warp's votes below only leave out forms that none of its rows needs.
+          const bool narrow = CAP && mg * sy <= 0.375f, wide = CAP && mg * sy <= 1.0f;
+          auto coefficients = [&](float (&co)[7]) {
+#pragma unroll
+            for (int k = 0; k < 7; ++k) co[k] = narrow ? (k < 4 ? a.narrow[k].x : 0.0f) : a.wide[k];
+          };
+          float m2 = mx == -INFINITY ? -INFINITY : mx * sc;
+          if (CAP && maxima) {
+            float co[7];
+            coefficients(co);
+            m2 = mx == -INFINITY ? -INFINITY : wide ? mx * ds_f2lo(ta_poly(co, ds_f2(mx, mx))) : ta_tanh(mx * sc, cap2);
+          }
           // (the bound again, so that a row does the same whoever made its warp look for maxima)
-          const bool up = m2 > mref && (!CAP || fminf(cap2, mg * lin) > mref);
+          const bool up = m2 > mref && (!CAP || (maxima && fminf(cap2, mg * lin) > mref));
           if (__any_sync(0xFFFFFFFFu, up)) {
             const float to = m2 + TA_ABOVE, f = up ? ta_ex2(mref - to) : 1.0f;     // 0 from -inf
             if (has) {
@@ -585,9 +589,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           }
           const float mu = mref == -INFINITY ? 0.0f : mref;
           const uint64_t nm2 = ds_f2(-mu, -mu);
-          // the polynomials where every score of the warp is well below the cap, else the exponential form
-          const bool narrow = CAP && __all_sync(0xFFFFFFFFu, mg * sy <= 0.375f);
-          const bool wide = CAP && __all_sync(0xFFFFFFFFu, mg * sy <= 1.0f);
+          const bool all_narrow = CAP && __all_sync(0xFFFFFFFFu, narrow), all_wide = CAP && __all_sync(0xFFFFFFFFu, wide);
+          const bool any_wide = CAP && __any_sync(0xFFFFFFFFu, wide);
           uint64_t sum[4] = {0, 0, 0, 0}, sum16[2] = {0, 0};
           auto put = [&](const uint64_t (&x)[8], int c) {      // weights of 16 keys: exponentials, sums, P
             uint32_t w[8];
@@ -607,7 +610,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
               x[e] = ds_fma2(y, CAP ? ta_poly_narrow(a, y) : ds_f2(sc, sc), nm2);
             }
           };
-          if (!CAP || (narrow && !masked)) {
+          if (!CAP || (all_narrow && !masked)) {
             // 16 keys' FMAs beside the 16 keys' exponentials before them: one warp alone keeps both pipes busy
             uint64_t x[2][8];
             ta_arrived(v);
@@ -623,21 +626,25 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
               put(x[c & 1], c);
             }
           } else {
+            float co[7];
+            coefficients(co);
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
-              uint64_t x[8];
+              uint64_t x[8] = {};
               ta_arrived(v);
-              if (narrow) {
-                exponents(x);
-              } else if (wide) {
+              if (any_wide) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                   const uint64_t y = ds_f2(v[2 * e], v[2 * e + 1]);
-                  x[e] = ds_fma2(y, ta_poly_wide(a, y), nm2);
+                  x[e] = ds_fma2(y, ta_poly(co, y), nm2);
                 }
-              } else {
+              }
+              if (!all_wide) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = ds_f2(ta_tanh(v[2 * e] * sc, cap2) - mu, ta_tanh(v[2 * e + 1] * sc, cap2) - mu);
+                for (int e = 0; e < 8; ++e) {
+                  const float x0 = ta_tanh(v[2 * e] * sc, cap2) - mu, x1 = ta_tanh(v[2 * e + 1] * sc, cap2) - mu;
+                  x[e] = wide ? x[e] : ds_f2(x0, x1);
+                }
               }
               if (masked) {
                 const uint32_t bits = ta_mask32(a, p.r, i, n, nd + 16 * c);
@@ -906,7 +913,7 @@ void ta_tanh_coefficients(TaArgs& a, float scale, float cap) {
   const double sy = double(scale) / cap;
   double f = sy * cap * 1.4426950408889634;
   for (int k = 0; k < 7; ++k, f *= sy * sy) {
-    a.wide[k] = make_float2(float(p[k] * f), float(p[k] * f));
+    a.wide[k] = float(p[k] * f);
     if (k < 4) a.narrow[k] = make_float2(float(q[k] * f), float(q[k] * f));
   }
 }

@@ -24,7 +24,8 @@ struct TaArgs {
   int32_t kt;                  // keys per tile
   int32_t box;                 // keys per copy (tensor-core kernel)
   float scale, softcap;
-  float2 wide[7], narrow[4];   // coefficients of the cap's polynomials, each twice
+  float wide[7];               // coefficients of the cap's polynomials,
+  float2 narrow[4];            // the short one's each twice
   int32_t* pref;               // [R + 1] running sum of the requests' tile counts
   float4* part_ml;             // [slots][rs] (reference in log2 units, sum of the weights, sum the result is divided by)
   float* part_o;               // [slots][rs][D] sums of weights times values, relative to the maximum

@@ -229,3 +229,10 @@ def test_caps_far_from_the_scores(dtype, T, softcap):
     """A cap far above the scores is no cap; one far below them leaves the signs."""
     c = Case(11, T, 4, 2, 64, 16, [600, 31], None, dtype, softcap=softcap).run()
     against_oracle(c, (0, 1), None if T < 10 else [0, 1, 35, T - 1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("softcap", [4.0, 30.0, 1e6])
+@pytest.mark.parametrize("T,Hq", [(9, 4), (70, 4)])
+def test_what_is_not_seen_changes_no_bit_under_a_cap(dtype, softcap, T, Hq):
+    same_bits_whatever_is_not_seen(dtype, softcap, T, Hq)
