@@ -26,6 +26,8 @@
 //   64 requests of one token x 4 heads, 300-8,200 keys 189 us   6.0 TB/s, 0.88
 //   4 trees of 64 nodes x 8 heads, 40,000-65,600 keys  193 us   982 TFLOP/s; with a cap 260 us, 730 TFLOP/s
 //   one token x 4 heads, 4,097 keys                     16 us   two tiles a block: latency
+#include <cmath>
+
 #include "tree_attn.cuh"
 
 extern "C" size_t dspark_internal_ws_tree_attention(int64_t R, int32_t T, int64_t cols, int32_t heads);
@@ -134,8 +136,8 @@ DS_DEV void ta_arrived(float (&v)[16]) {
 
 // cap2 * tanh(sy * s) = s * Q(s^2): tanh(y) = y P(y^2) with the coefficients of P that make the largest
 // relative error smallest (fitted by reweighted least squares), scaled by the powers of sy and by cap2; two
-// values at a time. Seven coefficients serve |y| <= 1 and four |y| <= 0.375; as evaluated in float32 their
-// errors are 1.6e-7 and 1.5e-7. The scaled coefficients are kernel arguments, made by ta_tanh_coefficients (the narrow
+// values at a time. Seven coefficients serve |y| <= 1 and four |y| <= 0.375 (wide_to, narrow_to: less where coefficients
+// leave float32's range); as evaluated in float32 their errors are 1.6e-7 and 1.5e-7. The scaled coefficients are kernel arguments, made by ta_tanh_coefficients (the narrow
 // ones a pair of each).
 DS_DEV uint64_t ta_pair(float2 x) { return ds_f2(x.x, x.y); }
 DS_DEV uint64_t ta_poly(const float (&co)[7], uint64_t s) {   // a row's own: the wide ones, or the narrow ones and zeros
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
     const int g = (warp - 4) >> 2, quarter = warp & 3, lr = quarter * 32 + lane;
     const uint32_t tl = tmem + (uint32_t(quarter * 32) << 16);
     const uint32_t tS = tl + TS + 128 * g, tO = tl + TO + DP * g;
-    const float sc = CAP ? a.scale * 2.0f * TA_LOG2E / a.softcap : a.scale * TA_LOG2E;
+    const float sc = CAP ? fminf(a.scale * 2.0f * TA_LOG2E / a.softcap, 3e38f) : a.scale * TA_LOG2E;   // finite: 0 stays 0
     const float cap2 = a.softcap * TA_LOG2E, sy = CAP ? a.scale / a.softcap : 0.0f;
     const float lin = a.scale * TA_LOG2E;                      // |capped score| <= min(cap, |score|)
     const int D = a.c.head_dim;
@@ -568,7 +570,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           ta_tmem_fetch(tS, v);
           // A row's form of the cap goes by the scores that it sees, so that its result is the same whatever the others
           // are; the warp's votes below only leave out forms that none of its rows needs.
-          const bool narrow = CAP && mg * sy <= 0.375f, wide = CAP && mg * sy <= 1.0f;
+          const bool narrow = CAP && mg * sy <= a.narrow_to, wide = CAP && (narrow || mg * sy <= a.wide_to);
           auto coefficients = [&](float (&co)[7]) {
 #pragma unroll
             for (int k = 0; k < 7; ++k) co[k] = narrow ? (k < 4 ? a.narrow[k].x : 0.0f) : a.wide[k];
@@ -913,11 +915,22 @@ void ta_tanh_coefficients(TaArgs& a, float scale, float cap) {
   static const double q[4] = {0x1.fffffep-1, -0x1.5551c6p-2, 0x1.10110cp-3, -0x1.8b7242p-5};
   if (!(cap > 0.0f)) return;
   const double sy = double(scale) / cap;
-  double f = sy * cap * 1.4426950408889634;
-  for (int k = 0; k < 7; ++k, f *= sy * sy) {
-    a.wide[k] = float(p[k] * f);
-    if (k < 4) a.narrow[k] = make_float2(float(q[k] * f), float(q[k] * f));
-  }
+  // How far a form serves. A coefficient that is no normal float32 number is 0: one too small belongs to a large cap, and
+  // below the limit its term is less than 2^-24 of the sum; one too large belongs to a tiny cap, which the exponential
+  // form serves whatever the score.
+  const auto scaled = [&](const double* co, int n, float most, auto put) {
+    double f = sy * cap * 1.4426950408889634;
+    double limit = most;
+    for (int k = 0; k < n; ++k, f *= sy * sy) {
+      const double x = std::fabs(co[k] * f);
+      if (!(x <= 0x1p127)) limit = -1.0;
+      else if (x < 0x1p-126) limit = std::min(limit, k ? std::pow(0x1p-24 / std::fabs(co[k]), 0.5 / k) : -1.0);
+      put(k, x >= 0x1p-126 && x <= 0x1p127 ? float(co[k] * f) : 0.0f);
+    }
+    return float(limit);
+  };
+  a.wide_to = scaled(p, 7, 1.0f, [&](int k, float x) { a.wide[k] = x; });
+  a.narrow_to = scaled(q, 4, 0.375f, [&](int k, float x) { a.narrow[k] = make_float2(x, x); });
 }
 
 constexpr size_t TA_WS_PREF = 4352;        // pref[TA_MAXR + 1], rounded up to 256 bytes

@@ -26,6 +26,7 @@ struct TaArgs {
   float scale, softcap;
   float wide[7];               // coefficients of the cap's polynomials,
   float2 narrow[4];            // the short one's each twice
+  float wide_to, narrow_to;    // and up to which |score| / cap they serve
   int32_t* pref;               // [R + 1] running sum of the requests' tile counts
   float4* part_ml;             // [slots][rs] (reference in log2 units, sum of the weights, sum the result is divided by)
   float* part_o;               // [slots][rs][D] sums of weights times values, relative to the maximum

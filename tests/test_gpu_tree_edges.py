@@ -236,3 +236,26 @@ def test_caps_far_from_the_scores(dtype, T, softcap):
 @pytest.mark.parametrize("T,Hq", [(9, 4), (70, 4)])
 def test_what_is_not_seen_changes_no_bit_under_a_cap(dtype, softcap, T, Hq):
     same_bits_whatever_is_not_seen(dtype, softcap, T, Hq)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("softcap", [1e-45, 1e-38, 1e-20, 1e-7, 1e-3])
+def test_scores_of_nothing_under_tiny_caps(dtype, softcap):
+    """Queries of zeros and keys of zeros beside others: every score is the cap, its negative or 0, the mean is the plain one."""
+    c = Case(14, 6, 4, 2, 64, 16, [300, 0], None, dtype, softcap=softcap)
+    c.q[0, 1], c.q[1, 0], c.q[0, 3, 1] = 0.0, 0.0, 0.0
+    c.k[place(c, 0, 7)], c.k[place(c, 1, 2)] = 0.0, 0.0
+    c.run()
+    against_oracle(c, (0, 1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("softcap", [0.5, 30.0, 300.0, 1e3, 1e4, 1e6])
+@pytest.mark.parametrize("top", [0.01, 0.2, 0.36, 0.7, 0.97, 3.0])
+def test_scores_up_to_and_past_the_cap(dtype, softcap, top):
+    """The largest score at a share of the cap, others from as far below zero: every form of the cap up to its end."""
+    c = Case(15, 3, 4, 2, 64, 16, [300], None, dtype, mask="chain", scale=0.125, softcap=softcap)
+    for h in range(2):
+        along(c, 0, h, np.linspace(-top, top, 300) * softcap)
+    c.run()
+    against_oracle(c, (0,))
