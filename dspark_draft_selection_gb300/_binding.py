@@ -124,10 +124,17 @@ def _dt(t) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
+# The current stream's handle without a Stream object for every call (a microsecond), where torch has the two functions:
+# they are not part of its public interface.
+_raw_stream, _device = (getattr(torch._C, f, None) for f in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+
+
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())   # no Stream object for every call
+    if _raw_stream is None or _device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_device())
 
 
 def _rows(t):

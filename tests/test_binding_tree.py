@@ -44,3 +44,26 @@ def test_the_tables_row_stride_is_passed_on(table, ld, monkeypatch):
             monkeypatch.undo()
             call()
         assert "device tensors" in str(e.value)
+
+
+class _Stream:
+    cuda_stream = 77
+
+
+@pytest.mark.parametrize("missing", ["_raw_stream", "_device"])
+def test_the_current_stream_without_torchs_own_functions(missing, monkeypatch):
+    """A torch without them: the public call gives the handle."""
+    monkeypatch.setattr(ds._binding, missing, None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: _Stream())
+    assert ds._binding._stream(None) == 77
+    other = _Stream()
+    other.cuda_stream = 5
+    assert ds._binding._stream(other) == 5
+
+
+@pytest.mark.gpu
+def test_the_current_streams_handle():
+    side = torch.cuda.Stream()
+    assert ds._binding._stream(None) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(side):
+        assert ds._binding._stream(None) == side.cuda_stream
