@@ -415,7 +415,8 @@ dspark_status dspark_grouped_conv(const void* x, dspark_dtype dtype, int64_t N, 
  * h * head_stride + d (strides in elements, >= 0). Slot s of request r is place s % page_size of
  * page page_table[r * ld_table + s / page_size] (int32 device, ids 0..num_pages - 1; table_pages
  * entries to a row). A slot past the table's row, or a page id out of range, sets DSPARK_ERANGE on *dev_status: nothing is written
- * there, and attention reads zeros. page_size 1..65536, heads >= 1, head_dim a multiple of 8,
+ * there. Attention reads zeros where a page id is out of range and leaves out slots past the table's row: nobody sees
+ * them, and nodes that belong there give zeros and lse = -inf. page_size 1..65536, heads >= 1, head_dim a multiple of 8,
  * 8..256.
  */
 typedef struct {

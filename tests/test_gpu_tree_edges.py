@@ -16,9 +16,9 @@ def place(c, r, j):
     return int(c.table[r, j // c.page]), j % c.page
 
 
-def against_oracle(c, requests, rows=None):
+def against_oracle(c, requests, rows=None, status=0):
     """Every element of the result, infinities with their sign and what is not a number included."""
-    assert int(c.status) == 0
+    assert int(c.status) == status
     for r in requests:
         ctx, n = c.ctx[r], c.n[r]
         i = np.arange(c.T) if rows is None else np.array(rows)
@@ -259,3 +259,49 @@ def test_scores_up_to_and_past_the_cap(dtype, softcap, top):
         along(c, 0, h, np.linspace(-top, top, 300) * softcap)
     c.run()
     against_oracle(c, (0,))
+
+
+# --- many requests, slots without a place ---
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,T,Hq,H,D", [(63, 3, 2, 1, 64), (64, 3, 2, 1, 64), (65, 3, 4, 2, 64), (200, 2, 4, 2, 128), (1024, 2, 2, 1, 64)])
+def test_many_requests(dtype, R, T, Hq, H, D):
+    """Ragged lengths, empty requests at the ends and among the others, up to the most requests of a call."""
+    rng = np.random.default_rng(R)
+    ctx, n = rng.integers(0, 300, R), rng.integers(0, T + 1, R)
+    ctx[rng.random(R) < 0.2], n[rng.random(R) < 0.2] = 0, 0
+    ctx[[0, R - 1]], n[[0, R - 1]] = 0, 0
+    c = Case(R, T, Hq, H, D, 16, ctx.tolist(), n.tolist(), dtype).run()
+    against_oracle(c, range(R))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_pages_out_of_range_read_as_zeros(dtype):
+    """Keys and values of such slots, committed or a node's, are zeros: scores of 0, nothing added."""
+    c = Case(2, 6, 4, 2, 64, 16, [100, 40], None, dtype)
+    table, pages = c.table.clone(), c.k.shape[0]
+    for bad in (-1, pages, 2 ** 31 - 1):
+        for page, whole in ((2, 0), (6, 0), (0, 1)):         # slots 32..47 and the nodes' of request 0, the first of request 1
+            c.table[whole, page] = bad
+            c.run()
+            assert int(c.status) == 2
+            c.table.copy_(table)
+            at = int(table[whole, page])
+            kept = c.k[at].clone(), c.v[at].clone()
+            c.k[at], c.v[at] = 0, 0                          # what the oracle reads there
+            against_oracle(c, (0, 1), status=2)
+            c.k[at], c.v[at] = kept
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_slots_past_the_tables_row_are_left_out(dtype):
+    """Committed slots past it are not seen, nodes there give zeros and -inf, the nodes before them do not see those."""
+    c = Case(3, 6, 4, 2, 64, 16, [90, 40], None, dtype, mask="block")
+    places = c.table.shape[1] * 16
+    good = c.run().out.clone()
+    for ctx, left in ((places - 6, 6), (places - 4, 4), (places, 0), (places + 5, 0), (10 ** 9, 0), (2 ** 31 - 1, 0)):
+        c.ctx = [ctx, 40]
+        c.run()
+        c.ctx, c.n = [min(ctx, places), 40], [left, 6]
+        against_oracle(c, (0, 1), status=0 if left == 6 else 2)
+        assert torch.equal(c.out[1], good[1]) and not c.out[0, left:].any() and torch.all(c.lse[0, left:] == -float("inf"))
+        c.n = [6, 6]
