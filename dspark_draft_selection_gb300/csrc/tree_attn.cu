@@ -218,22 +218,32 @@ DS_DEV void ta_clean(uint8_t* st, int f, int k0, int k1, int node, uint32_t* odd
 __device__ __noinline__ void ta_add_odd(const TaArgs& a, int r, int32_t ctx, int32_t n, int i, int hk, int d0, int d1,
                                         const uint32_t* odd, __nv_bfloat16* out, float* part) {
   const __nv_bfloat16* vc = reinterpret_cast<const __nv_bfloat16*>(a.c.v) + hk * a.c.head_stride;
-  for (int w = 0; w < a.W; ++w) {
-    if (odd[w] == 0u) continue;
-    for (uint32_t bits = odd[w] & ta_mask32(a, r, i, n, 32 * w); bits; bits &= bits - 1) {
-      const int64_t at = ta_slot(a, r, int64_t(ctx) + 32 * w + __ffs(int(bits)) - 1);
-      if (at < 0) continue;
-      for (int d = d0; d < d1; d += 8) {
-        const uint4 y = *reinterpret_cast<const uint4*>(vc + at + d);
-        const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+  for (int d = d0; d < d1; d += 32) {                  // 32 columns for one lookup of a node's slot
+    float z[32] = {};
+    for (int w = 0; w < a.W; ++w) {
+      if (odd[w] == 0u) continue;
+      for (uint32_t bits = odd[w] & ta_mask32(a, r, i, n, 32 * w); bits; bits &= bits - 1) {
+        const int64_t at = ta_slot(a, r, int64_t(ctx) + 32 * w + __ffs(int(bits)) - 1);
+        if (at < 0) continue;
+        uint32_t x[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (!(ta_odd(x[e >> 1]) & (e & 1 ? 0x80000000u : 0x8000u))) continue;
-          const float z = __uint_as_float(e & 1 ? x[e >> 1] & 0xFFFF0000u : x[e >> 1] << 16);
-          if (out) out[d + e] = __float2bfloat16_rn(__bfloat162float(out[d + e]) + z);
-          else part[d + e] += z;
+        for (int e = 0; e < 4; ++e) {
+          const uint4 y = d + 8 * e < d1 ? *reinterpret_cast<const uint4*>(vc + at + d + 8 * e) : make_uint4(0, 0, 0, 0);
+          x[4 * e] = y.x; x[4 * e + 1] = y.y; x[4 * e + 2] = y.z; x[4 * e + 3] = y.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t bad = ta_odd(x[e]);
+          z[2 * e] += bad & 0x8000u ? __uint_as_float(x[e] << 16) : 0.0f;
+          z[2 * e + 1] += bad & 0x80000000u ? __uint_as_float(x[e] & 0xFFFF0000u) : 0.0f;
         }
       }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      if (z[e] == 0.0f || d + e >= d1) continue;       // what is not a number is not 0
+      if (out) out[d + e] = __float2bfloat16_rn(__bfloat162float(out[d + e]) + z[e]);
+      else part[d + e] += z[e];
     }
   }
 }

@@ -105,15 +105,11 @@ def test_every_node_with_values_that_are_not_finite():
     against_oracle(c, (0,), [0, 1, 2, 3, 4, 250, 252, 510, 511])
 
 
-@pytest.mark.parametrize("T,Hq", [(8, 8), (64, 8)])
-@pytest.mark.parametrize("where", ["committed", "node"])
-def test_a_value_that_is_not_finite_takes_no_longer(T, Hq, where):
-    """One bad value in one request of many, whose items have one block each: the call's time is a clean call's
-    (three times as much at most, for the clocks' sake)."""
+def times(T, Hq, bad, R=80, ctx=2000):
+    """(best time of a clean call, of one with `bad` done to the case, the two results) of requests whose items have one block each."""
     import dspark_draft_selection_gb300 as ds
-    R = 80
-    c = Case(3, T, Hq, 2, 64, 16, [2000] * R, None, mask="chain")
-    ctx = torch.tensor(c.ctx, dtype=torch.int32, device="cuda")
+    c = Case(3, T, Hq, 2, 64, 16, [ctx] * R, None, mask="chain")
+    lens = torch.tensor(c.ctx, dtype=torch.int32, device="cuda")
     ws, st, out = ds.workspace(ds.OP_TREE_ATTENTION, R, T, Hq * 64, 2), ds.new_status(), torch.empty_like(c.q)
 
     def took():
@@ -122,18 +118,41 @@ def test_a_value_that_is_not_finite_takes_no_longer(T, Hq, where):
             a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
             torch.cuda.synchronize()
             a.record()
-            ds.dspark_tree_attention(c.q, c.k, c.v, c.table, ctx, out=out, ws=ws, status=st)
+            ds.dspark_tree_attention(c.q, c.k, c.v, c.table, lens, out=out, ws=ws, status=st)
             b.record()
             torch.cuda.synchronize()
             best = min(best, a.elapsed_time(b))
         return best
 
-    clean = took()
-    good = out.clone()
-    c.v[place(c, 41, 700 if where == "committed" else 2001)] = float("nan")
+    clean, good = took(), out.clone()
+    bad(c)
     got = took()
-    assert int(st) == 0 and torch.isnan(out[41].float()).any() and torch.equal(out[:41], good[:41]) and torch.equal(out[42:], good[42:])
+    assert int(st) == 0
+    return clean, got, good, out
+
+
+@pytest.mark.parametrize("T,Hq", [(8, 8), (64, 8)])
+@pytest.mark.parametrize("where", ["committed", "node"])
+def test_a_value_that_is_not_finite_takes_no_longer(T, Hq, where):
+    """One bad value in one request of many: the call's time is a clean call's (three times as much at most, for the
+    clocks' sake)."""
+    def bad(c):
+        c.v[place(c, 41, 700 if where == "committed" else 2001)] = float("nan")
+
+    clean, got, good, out = times(T, Hq, bad)
+    assert torch.isnan(out[41].float()).any() and torch.equal(out[:41], good[:41]) and torch.equal(out[42:], good[42:])
     assert got < 3 * clean, (got, clean)
+
+
+def test_a_tree_of_values_that_are_not_finite_takes_little_longer():
+    """All 64 nodes of one request, each of which up to 64 rows see (as a model that broke down leaves them)."""
+    def bad(c):
+        for j in range(2000, 2064):
+            c.v[place(c, 41, j)] = float("nan")
+
+    clean, got, good, out = times(64, 8, bad)
+    assert torch.isnan(out[41].float()).all() and torch.equal(out[:41], good[:41]) and torch.equal(out[42:], good[42:])
+    assert got < 5 * clean, (got, clean)
 
 
 # --- what is not seen ---
