@@ -124,16 +124,21 @@ def _dt(t) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
-# The current stream's handle without a Stream object for every call (a microsecond), where torch has the two functions:
-# they are not part of its public interface.
-_raw_stream, _device = (getattr(torch._C, f, None) for f in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+def _stream_calls(c):
+    """(handle of a device's current stream, the current device): torch's own functions, which make no Stream object for
+    every call (a microsecond) but are not part of its public interface; without them the public call."""
+    raw, device = (getattr(c, f, None) for f in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is None or device is None:
+        return (lambda _: torch.cuda.current_stream().cuda_stream), (lambda: None)
+    return raw, device
+
+
+_raw_stream, _device = _stream_calls(torch._C)
 
 
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is None or _device is None:
-        return torch.cuda.current_stream().cuda_stream
     return _raw_stream(_device())
 
 

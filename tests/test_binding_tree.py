@@ -50,10 +50,12 @@ class _Stream:
     cuda_stream = 77
 
 
-@pytest.mark.parametrize("missing", ["_raw_stream", "_device"])
-def test_the_current_stream_without_torchs_own_functions(missing, monkeypatch):
-    """A torch without them: the public call gives the handle."""
-    monkeypatch.setattr(ds._binding, missing, None)
+@pytest.mark.parametrize("has", [(), ("_cuda_getDevice",), ("_cuda_getCurrentRawStream",)])
+def test_the_current_stream_without_torchs_own_functions(has, monkeypatch):
+    """A torch without both of them: the public call gives the handle."""
+    raw, device = ds._binding._stream_calls(type("C", (), {f: staticmethod(lambda *_: 3) for f in has}))
+    monkeypatch.setattr(ds._binding, "_raw_stream", raw)
+    monkeypatch.setattr(ds._binding, "_device", device)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda: _Stream())
     assert ds._binding._stream(None) == 77
     other = _Stream()
