@@ -53,10 +53,10 @@ DS_DEV void ra_set(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
 // of both halves of a rotated head, VEC columns a head passes through unrotated, or VEC columns of a value
 // head. VEC * sizeof(T) is 16 bytes where the layout allows, then four elements, else one. With few rows
 // grid.y splits the items of a row.
-// 12,002 rows of 32 + 2 x 8 heads of 128 bf16 columns, three axes: 46.9 us, 5.4 TB/s of the bytes that have to
-// move. What carries it is the number of blocks an SM holds (12, at 40 registers), since each waits for its
-// page and its table rows before it moves anything: blocks of 256 threads with four rows 49-51 us, items two
-// and three at a time (fewer blocks) 55 and 66 us, eight rows a block 58-64 us.
+// 12,002 rows of 32 + 2 x 8 heads of 128 bf16 columns, three axes: 45.9 us, 5.6 TB/s of the bytes that have to
+// move (float32: 85.7 us, 5.9 TB/s). What carries it is the number of blocks an SM holds (12, at 40 registers), since
+// each waits for its page and its table rows before it moves anything: blocks of 256 threads with four rows 49-51 us,
+// items two and three at a time (fewer blocks) 55 and 66 us, eight rows a block 58-64 us.
 template <typename T, int VEC, int NR>
 __global__ void __launch_bounds__(RA_THREADS, NR > 1 ? 12 : 1) rope_append_kernel(const RaArgs a) {
   using V = RaVec<T, VEC>;

@@ -22,9 +22,9 @@
 // Bound: HBM (2 D bytes of keys and of values per cached token and key head) up to about 128 query rows per
 // key head, above that the chain P V, Q K^T, softmax of a group: S and P share their tensor memory (S, O of
 // both groups take all 512 columns), so a group's next scores wait for its P V. Measured with the join:
-//   32 requests of 8 nodes x 4 heads, 300-8,200 keys   112 us   5.1 TB/s, 0.75 of the measured copy rate
+//   32 requests of 8 nodes x 4 heads, 300-8,200 keys   113 us   5.1 TB/s, 0.75 of the measured copy rate
 //   64 requests of one token x 4 heads, 300-8,200 keys 189 us   6.0 TB/s, 0.88
-//   4 trees of 64 nodes x 8 heads, 40,000-65,600 keys  193 us   982 TFLOP/s; with a cap 260 us, 730 TFLOP/s
+//   4 trees of 64 nodes x 8 heads, 40,000-65,600 keys  198 us   959 TFLOP/s; with a cap 250 us, 760 TFLOP/s
 //   one token x 4 heads, 4,097 keys                     16 us   two tiles a block: latency
 #include <cmath>
 
@@ -978,7 +978,8 @@ extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64
   a.rows = T * a.G; a.scale = scale; a.softcap = softcap; a.status = dev_status; a.first_wait = g_ds_first_wait_polls.load();
   int box = 128;
   while (cache->page_size % box) box >>= 1;
-  // (32 requests of 8 nodes, 300-8,200 keys: 109 us, in float32 arithmetic 678 us.)
+  // (32 requests of 8 nodes, 300-8,200 keys: 113 us, in float32 arithmetic 681 us; with 256 columns, which only that
+  // takes, 2,404 us.)
   // Tensor cores: rows of bf16 that TMA can copy (16-byte rows; eight places of a page are the smallest box
   // whose swizzle starts on its own pattern) and outputs that 16-byte stores can write.
   const bool tc = cache->dtype == DSPARK_BF16 && D <= 128 && box >= 8 && ds_cache_vec(cache) && ds_aligned(q, 16) &&
@@ -992,8 +993,8 @@ extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64
   a.box = box;
   if (maps) {
     // Two row tiles a block where there are more than 128 rows, so that a key tile is read once for both: 160,
-    // 256 and 512 rows (4 requests, 40,000-65,600 keys) 101, 118 and 194 us, with one row tile a block 124, 128
-    // and 244 us.
+    // 256 and 512 rows (4 requests, 40,000-65,600 keys) 101, 118 and 198 us, with one row tile a block 128, 131
+    // and 248 us.
     a.rpg = a.rows > 128 ? 256 : 128;
   } else {                                             // groups of 64 rows or fewer, as even as sixteens allow
     const int64_t groups = ds_ceil_div(a.rows, 64);
@@ -1009,7 +1010,7 @@ extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64
   a.pref = reinterpret_cast<int32_t*>(w);
   a.part_o = reinterpret_cast<float*>(w + TA_WS_PREF);
   a.part_ml = reinterpret_cast<float4*>(a.part_o + slots * a.rs * D);
-  // 64 columns have their own form: 64 rows 52.6 us, 512 rows 165 us, padded to 128 columns 57.8 and 178 us.
+  // 64 columns have their own form: 64 rows 54.6 us, 512 rows 167 us, padded to 128 columns 60.5 and 183 us.
   if (maps) DS_CUDA_TRY(D <= 64 ? ta_dispatch_tc<64>(a, grid, mk, mv, stream) : ta_dispatch_tc<128>(a, grid, mk, mv, stream));
   else DS_CUDA_TRY(ta_launch_float(a, grid, stream));
   const dim3 jg{unsigned(ds_ceil_div(jobs, 8))}, jb{256};
