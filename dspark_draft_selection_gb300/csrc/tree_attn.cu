@@ -213,11 +213,28 @@ DS_DEV void ta_clean(uint8_t* st, int f, int k0, int k1, int node, uint32_t* odd
 }
 
 // What nodes whose values are not finite add to a row that sees them: a weight is more than 0, so its product with an
-// infinity or with what is not a number is that value itself. One thread a row; `out` (the result) or `part` (a
-// partial one) holds the row without them, this thread having written columns [d0, d1).
+// infinity or with what is not a number is that value itself - unless the score is -inf, whose weight 0 makes it not a
+// number. One thread a row; `out` (the result) or `part` (a partial one) holds the row without them, this thread having
+// written columns [d0, d1); `q` is its query.
 __device__ __noinline__ void ta_add_odd(const TaArgs& a, int r, int32_t ctx, int32_t n, int i, int hk, int d0, int d1,
-                                        const uint32_t* odd, __nv_bfloat16* out, float* part) {
+                                        const uint32_t* odd, const __nv_bfloat16* q, __nv_bfloat16* out, float* part) {
+  const __nv_bfloat16* kc = reinterpret_cast<const __nv_bfloat16*>(a.c.k) + hk * a.c.head_stride;
   const __nv_bfloat16* vc = reinterpret_cast<const __nv_bfloat16*>(a.c.v) + hk * a.c.head_stride;
+  uint32_t none[TA_MAXT / 32] = {};                    // nodes of weight 0; no capped score is -inf
+  for (int w = 0; w < a.W && a.softcap == 0.0f; ++w) {
+    if (odd[w] == 0u) continue;
+    for (uint32_t bits = odd[w] & ta_mask32(a, r, i, n, 32 * w); bits; bits &= bits - 1) {
+      const int64_t at = ta_slot(a, r, int64_t(ctx) + 32 * w + __ffs(int(bits)) - 1);
+      if (at < 0) continue;
+      float s = 0.0f;
+      for (int d = 0; d < a.c.head_dim; d += 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(q + d), y = *reinterpret_cast<const uint4*>(kc + at + d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = __fmaf_rn(ds_vec_elem<__nv_bfloat16>(x, e), ds_vec_elem<__nv_bfloat16>(y, e), s);
+      }
+      if (s == -INFINITY) none[w] |= bits & (0u - bits);
+    }
+  }
   for (int d = d0; d < d1; d += 32) {                  // 32 columns for one lookup of a node's slot
     float z[32] = {};
     for (int w = 0; w < a.W; ++w) {
@@ -225,6 +242,7 @@ __device__ __noinline__ void ta_add_odd(const TaArgs& a, int r, int32_t ctx, int
       for (uint32_t bits = odd[w] & ta_mask32(a, r, i, n, 32 * w); bits; bits &= bits - 1) {
         const int64_t at = ta_slot(a, r, int64_t(ctx) + 32 * w + __ffs(int(bits)) - 1);
         if (at < 0) continue;
+        const float times = none[w] & bits & (0u - bits) ? 0.0f : 1.0f;
         uint32_t x[16];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -234,8 +252,8 @@ __device__ __noinline__ void ta_add_odd(const TaArgs& a, int r, int32_t ctx, int
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const uint32_t bad = ta_odd(x[e]);
-          z[2 * e] += bad & 0x8000u ? __uint_as_float(x[e] << 16) : 0.0f;
-          z[2 * e + 1] += bad & 0x80000000u ? __uint_as_float(x[e] & 0xFFFF0000u) : 0.0f;
+          z[2 * e] += bad & 0x8000u ? __uint_as_float(x[e] << 16) * times : 0.0f;
+          z[2 * e + 1] += bad & 0x80000000u ? __uint_as_float(x[e] & 0xFFFF0000u) * times : 0.0f;
         }
       }
     }
@@ -770,7 +788,9 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_tc_kernel(const TaArg
           uint32_t marks = 0;
 #pragma unroll 1
           for (int w = 0; w < a.W; ++w) marks |= odd[w];
-          if (marks && valid) ta_add_odd(a, p.r, ctx, n, i, p.hk, d0, min(d1, D), odd, whole ? out : nullptr, part);
+          if (marks && valid)
+            ta_add_odd(a, p.r, ctx, n, i, p.hk, d0, min(d1, D), odd, reinterpret_cast<const __nv_bfloat16*>(a.q) + row * a.ldq + int64_t(h) * D,
+                       whole ? out : nullptr, part);
         }
       }
       // Marks of this piece's nodes. (Those of the piece before are no longer read: O was free for this piece after

@@ -105,6 +105,21 @@ def test_every_node_with_values_that_are_not_finite():
     against_oracle(c, (0,), [0, 1, 2, 3, 4, 250, 252, 510, 511])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,Hq", SIZES)
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_nodes_with_keys_and_values_that_are_not_finite(dtype, T, Hq, softcap):
+    """An infinity in a node's key makes scores of both signs: a weight of 0 (none under a cap) times an infinite value is not
+    a number, and the score of +inf spoils its row."""
+    c = Case(T + 1, T, Hq, 2, 64, 16, [300, 0], [T, T - 1], dtype, softcap=softcap)
+    for r, j, col, key, value in ((0, 1, 5, float("inf"), float("inf")), (0, 4, 9, -float("inf"), float("nan")),
+                                  (1, 3, 5, -float("inf"), -float("inf")), (1, 2, 0, float("inf"), 1.0)):
+        at = place(c, r, c.ctx[r] + j)
+        c.k[at][:, col], c.v[at][:, 2 * col + 3] = key, value
+    c.run()
+    against_oracle(c, (0, 1), None if T < 10 else list(range(12)) + [T - 2, T - 1])
+
+
 def times(T, Hq, bad, R=80, ctx=2000):
     """(best time of a clean call, of one with `bad` done to the case, the two results) of requests whose items have one block each."""
     import dspark_draft_selection_gb300 as ds
