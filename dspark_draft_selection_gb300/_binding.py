@@ -19,8 +19,9 @@ c_i32, c_i64, c_f32, c_vp, c_sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 DSPARK_BF16, DSPARK_F32 = 0, 1
 DSPARK_MAXSUM, DSPARK_WALK, DSPARK_SAMPLE = 0, 1, 2
+DSPARK_E4M3, DSPARK_INT8 = 0, 1
 OP_TOPK, OP_LATTICE, OP_CHAIN, OP_SAMPLE, OP_DENSE_WALK, OP_VERIFY, OP_D2T_CHECK, OP_LATTICE_ROW, \
-    OP_TREE_ATTENTION = range(9)
+    OP_TREE_ATTENTION, OP_TREE_ATTENTION_Q8 = range(10)
 STATUS = {0: "DSPARK_OK", 1: "DSPARK_EINVAL", 2: "DSPARK_ERANGE", 3: "DSPARK_EDUP", 4: "DSPARK_EPROPOSAL",
           5: "DSPARK_ENONFINITE", 6: "DSPARK_ETIMEOUT", 7: "DSPARK_ECUDA", 8: "DSPARK_EWORKSPACE"}
 MODES = {"maxsum": DSPARK_MAXSUM, "walk": DSPARK_WALK, "sample": DSPARK_SAMPLE}
@@ -58,6 +59,14 @@ SIGNATURES = [
                                       c_i64, c_vp, c_vp, c_sz, c_vp, c_vp]),
     ("dspark_tree_accept", c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
     ("dspark_cache_commit", c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp]),
+    ("dspark_rope_append_q8", c_i32, [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_i32, c_i32, c_vp, c_i32, c_vp,
+                                      c_i64, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp]),
+    ("dspark_tree_attention_q8", c_i32, [c_vp, c_i64, c_i32, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_f32, c_f32, c_vp,
+                                         c_i64, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    ("dspark_cache_commit_q8", c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp]),
+    ("dspark_cache_read_q8", c_i32, [c_vp, c_vp, c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_vp]),
+    ("dspark_tree_verify", c_i32, [c_vp, c_i64, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp,
+                                   c_vp, c_vp]),
 ]
 
 
@@ -77,6 +86,15 @@ class KVCache(ctypes.Structure):
     _fields_ = [("k", c_vp), ("v", c_vp), ("dtype", c_i32), ("n_layers", c_i32), ("layer_stride", c_i64),
                 ("page_stride", c_i64), ("token_stride", c_i64), ("head_stride", c_i64), ("num_pages", c_i64),
                 ("page_size", c_i32), ("heads", c_i32), ("head_dim", c_i32), ("page_table", c_vp), ("ld_table", c_i32), ("table_pages", c_i32)]
+
+
+class QCache(ctypes.Structure):
+    """dspark_qcache: a paged key/value cache in 8 bits (two buffers of codes, two of scales) and its page table."""
+    _fields_ = [("k", c_vp), ("v", c_vp), ("k_scale", c_vp), ("v_scale", c_vp), ("code", c_i32), ("n_layers", c_i32),
+                ("layer_stride", c_i64), ("page_stride", c_i64), ("token_stride", c_i64), ("head_stride", c_i64),
+                ("scale_layer_stride", c_i64), ("scale_page_stride", c_i64), ("scale_token_stride", c_i64),
+                ("scale_head_stride", c_i64), ("num_pages", c_i64), ("page_size", c_i32), ("heads", c_i32), ("head_dim", c_i32),
+                ("page_table", c_vp), ("ld_table", c_i32), ("table_pages", c_i32)]
 
 
 class DsparkError(RuntimeError):
@@ -439,6 +457,18 @@ _KV = struct.Struct("@" + "".join({c_vp: "P", c_i32: "i", c_i64: "q"}[t] for _, 
 _I32 = torch.int32
 
 
+def _table(page_table):
+    """(requests, entries of a row, row stride) of an int32 page table [R, n]."""
+    tsh, tst = page_table.shape, page_table.stride()
+    if len(tsh) != 2 or tst[1] != 1 or page_table.dtype is not _I32:
+        raise ValueError("expected an int32 page table [R, pages] with unit column stride")
+    R, entries = tsh
+    ld = tst[0] if R > 1 else entries                      # a single row's stride says nothing
+    if ld < entries:                                       # an expanded table: row r would be read past its end
+        raise ValueError("the page table's rows overlap: make it contiguous, or give every request its own row")
+    return R, entries, ld
+
+
 def _kvcache(k, v, page_table):
     """(bytes of a dspark_kvcache, heads, head_dim, requests) of k, v [(layers,) pages, page, heads, head_dim] (any
     strides, the last 1) and page_table [R, n]. Packed bytes cost a third of filling a ctypes structure."""
@@ -448,13 +478,7 @@ def _kvcache(k, v, page_table):
     n = len(st)
     if n not in (4, 5) or st[-1] != 1:
         raise ValueError("expected [(layers,) pages, page, heads, head_dim] with unit column stride")
-    tsh, tst = page_table.shape, page_table.stride()
-    if len(tsh) != 2 or tst[1] != 1 or page_table.dtype is not _I32:
-        raise ValueError("expected an int32 page table [R, pages] with unit column stride")
-    R, entries = tsh
-    ld = tst[0] if R > 1 else entries                      # a single row's stride says nothing
-    if ld < entries:                                       # an expanded table: row r would be read past its end
-        raise ValueError("the page table's rows overlap: make it contiguous, or give every request its own row")
+    R, entries, ld = _table(page_table)
     pages, page, H, D = sh[-4:]
     layers, lst = (sh[0], st[0]) if n == 5 else (1, 0)
     return _KV.pack(_p(k), _p(v), _dt(k), layers, lst, st[-4], st[-3], st[-2], pages, page, H, D, _p(page_table),
@@ -595,3 +619,170 @@ def dspark_cache_commit(k_cache, v_cache, page_table, ctx_len, path, n_accepted,
     _check(lib().dspark_cache_commit(c, _i32(ctx_len, R), _i32(path, R, T), _i32(n_accepted, R), R, T,
                                      _i32(out, R), _p(status), _stream(stream)), "dspark_cache_commit")
     return out, status
+
+
+_Q8 = struct.Struct("@" + "".join({c_vp: "P", c_i32: "i", c_i64: "q"}[t] for _, t in QCache._fields_))
+_CODES = {torch.float8_e4m3fn: DSPARK_E4M3, torch.int8: DSPARK_INT8}
+
+
+def q8_cache(pages, page, heads, head_dim, *, layers=None, dtype=torch.float8_e4m3fn, device="cuda"):
+    """An empty cache in 8 bits for the functions below: (k, v, k_scale, v_scale), the codes (float8_e4m3fn or int8)
+    [(layers,) pages, page, heads, head_dim], the scale bytes (uint8) [(layers,) pages, page, heads, blocks of 32 columns], a head's
+    slots side by side in a page."""
+    if dtype not in _CODES:
+        raise TypeError(f"codes are float8_e4m3fn or int8, not {dtype}")
+    lead = () if layers is None else (layers,)
+    codes = [torch.zeros(lead + (pages, page, heads, head_dim), dtype=torch.uint8, device=device).view(dtype) for _ in range(2)]
+    scales = [torch.ones(lead + (pages, heads, page, (head_dim + 31) // 32), dtype=torch.uint8, device=device).transpose(-3, -2)
+              for _ in range(2)]
+    return (*codes, *scales)
+
+
+def _qcache(cache, page_table):
+    """(bytes of a dspark_qcache, heads, head_dim, requests) of cache = (k, v, k_scale, v_scale) as q8_cache makes it (any strides, the
+    last 1) and page_table [R, n]."""
+    k, v, ks, vs = cache
+    sh, st, ssh, sst = k.shape, k.stride(), ks.shape, ks.stride()
+    if v.shape != sh or v.stride() != st or v.dtype is not k.dtype:
+        raise ValueError("keys and values are of one shape, layout and type")
+    if k.dtype not in _CODES:
+        raise TypeError(f"codes are float8_e4m3fn or int8, not {k.dtype}")
+    n = len(st)
+    if n not in (4, 5) or st[-1] != 1:
+        raise ValueError("expected codes [(layers,) pages, page, heads, head_dim] with unit column stride")
+    if ssh != (*sh[:-1], (sh[-1] + 31) // 32) or vs.shape != ssh or vs.stride() != sst or ks.dtype is not torch.uint8 or vs.dtype is not torch.uint8:
+        raise ValueError("expected uint8 scales [(layers,) pages, page, heads, blocks of 32 columns], keys' and values' of one layout")
+    if sst[-1] != 1 and ssh[-1] > 1:
+        raise ValueError("expected scales with unit block stride")
+    R, entries, ld = _table(page_table)
+    pages, page, H, D = sh[-4:]
+    layers, lst, slst = (sh[0], st[0], sst[0]) if n == 5 else (1, 0, 0)
+    return _Q8.pack(_p(k), _p(v), _p(ks), _p(vs), _CODES[k.dtype], layers, lst, st[-4], st[-3], st[-2], slst, sst[-4], sst[-3], sst[-2],
+                    pages, page, H, D, _p(page_table), ld, entries), H, D, R
+
+
+def dspark_rope_append_q8(q, k, v, pos, cos_sin, cache, page_table, ctx_len, *, axis=None, n_nodes=None, interleaved=False, out=None,
+                          status=None, stream=None):
+    """dspark_rope_append into a cache in 8 bits (q8_cache): turns q [R, T, Hq, D] and k [R, T, H, D] by their positions and writes k
+    and v, quantised, to the nodes' slots. Returns (q_out, status); out may be q itself."""
+    if stream is not None:
+        return _on(stream, dspark_rope_append_q8, locals())
+    qs = q.shape
+    R, T, Hq, D = qs
+    c, H, Dc, Rt = _qcache(cache, page_table)
+    if D != Dc or Rt != R:
+        raise ValueError("q, the cache and its page table do not fit together")
+    dt, ks = q.dtype, (R, T, H, D)
+    out = torch.empty(qs, dtype=dt, device=q.device) if out is None else out
+    status = new_status(q.device) if status is None else status
+    A = pos.shape[2] if pos.dim() == 3 else 1
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("expected a contiguous float32 table cos_sin [P, rot]")
+    P, rot = cos_sin.shape
+    _check(lib().dspark_rope_append_q8(_p(q), _node_rows(q, qs, dt), _p(k), _node_rows(k, ks, dt), _p(v), _node_rows(v, ks, dt),
+                                       _dt(q), R, T, Hq, _i32(pos, R, T, A) if pos.dim() == 3 else _i32(pos, R, T), A, _p(cos_sin), P,
+                                       rot, _i32(axis, rot // 2), int(interleaved), c, _i32(ctx_len, R), _i32(n_nodes, R), _p(out),
+                                       _node_rows(out, qs, dt), _p(status), _stream(stream)), "dspark_rope_append_q8")
+    return out, status
+
+
+def dspark_tree_attention_q8(q, cache, page_table, ctx_len, *, mask=None, n_nodes=None, scale=None, softcap=0.0, out=None, lse=None,
+                             ws=None, status=None, stream=None):
+    """dspark_tree_attention over a cache in 8 bits (q8_cache); T = 1: the attention of one new token a request, whose key and value
+    are in the cache. ws: workspace(OP_TREE_ATTENTION_Q8, R, T, Hq * D, H). Returns (out, lse, status)."""
+    if stream is not None:
+        return _on(stream, dspark_tree_attention_q8, locals())
+    qs = q.shape
+    R, T, Hq, D = qs
+    c, H, Dc, Rt = _qcache(cache, page_table)
+    if D != Dc or Rt != R:
+        raise ValueError("q, the cache and its page table do not fit together")
+    dt = q.dtype
+    out = torch.empty(qs, dtype=dt, device=q.device) if out is None else out
+    if lse is None:
+        lse = torch.empty((R, T, Hq), dtype=torch.float32, device=q.device)
+    elif lse is False:
+        lse = None
+    elif lse.shape != (R, T, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous():
+        raise ValueError("expected a contiguous float32 lse [R, T, Hq]")
+    status = new_status(q.device) if status is None else status
+    wp, wn = _ws(workspace(OP_TREE_ATTENTION_Q8, R, T, Hq * D, H, q.device) if ws is None else ws)
+    _check(lib().dspark_tree_attention_q8(_p(q), _node_rows(q, qs, dt), _dt(q), R, T, Hq, c, _i32(ctx_len, R), _i32(n_nodes, R),
+                                          _i32(mask, R, T, (T + 31) // 32), D ** -0.5 if scale is None else scale, softcap,
+                                          _p(out), _node_rows(out, qs, dt), _p(lse), wp, wn, _p(status), _stream(stream)),
+           "dspark_tree_attention_q8")
+    return out, lse, status
+
+
+def dspark_cache_commit_q8(cache, page_table, ctx_len, path, n_accepted, *, T=None, out=None, status=None, stream=None):
+    """dspark_cache_commit for a cache in 8 bits (q8_cache, every layer of it). Returns (new_len [R], status)."""
+    if stream is not None:
+        return _on(stream, dspark_cache_commit_q8, locals())
+    c, _, _, R = _qcache(cache, page_table)
+    if path is not None:
+        T = path.shape[1]
+    out = torch.empty((R,), dtype=torch.int32, device=ctx_len.device) if out is None else out
+    status = new_status(ctx_len.device) if status is None else status
+    _check(lib().dspark_cache_commit_q8(c, _i32(ctx_len, R), _i32(path, R, T), _i32(n_accepted, R), R, T,
+                                        _i32(out, R), _p(status), _stream(stream)), "dspark_cache_commit_q8")
+    return out, status
+
+
+def dspark_cache_read_q8(cache, page_table, n, *, start=None, S=None, dtype=torch.bfloat16, out=None, status=None, stream=None):
+    """Reads slots start[r] .. start[r] + n[r] - 1 of every request of a cache in 8 bits back: (k, v, status), k and v [R, S, H, D] of
+    `dtype` (bfloat16 or float32). S: rows a request has there; without `out` it has to be given, and rows past n[r] are then 0. out:
+    (k, v) of one layout, whose rows past n[r] are left as they were."""
+    if stream is not None:
+        return _on(stream, dspark_cache_read_q8, locals())
+    if out is None and S is None:
+        raise ValueError("S, the rows of a request, or out has to be given")
+    c, H, D, R = _qcache(cache, page_table)
+    if out is None:
+        out = tuple(torch.zeros((R, S, H, D), dtype=dtype, device=n.device) for _ in range(2))
+    k, v = out
+    if k.dim() != 4 or (S is not None and S != k.shape[1]):
+        raise ValueError("expected out of [R, S, heads, head_dim]")
+    S, shape = k.shape[1], (R, k.shape[1], H, D)
+    ld = _node_rows(k, shape, k.dtype)
+    if _node_rows(v, shape, k.dtype) != ld:
+        raise ValueError("keys and values are read into one layout")
+    status = new_status(n.device) if status is None else status
+    _check(lib().dspark_cache_read_q8(c, _i32(start, R), _i32(n, R), R, S, _dt(k), _p(k), _p(v), ld, _p(status), _stream(stream)),
+           "dspark_cache_read_q8")
+    return k, v, status
+
+
+def _rows3(t, R, T, V):
+    """Row stride of float32 probabilities [R, T, V] whose rows lie at one stride."""
+    if t.shape != (R, T, V) or t.dtype is not torch.float32:
+        raise ValueError(f"expected float32 probabilities {(R, T, V)}, got {t.dtype} {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and V > 1) or (s0 != T * s1 and R > 1 and T > 1):
+        raise ValueError("expected [R, T, V] with unit column stride and one row stride")
+    return s1 if T > 1 else s0 if R > 1 else V
+
+
+def _f64(t, *shape):
+    if t.dtype is not torch.float64 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"expected a contiguous float64 tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    return _p(t)
+
+
+def dspark_tree_verify(p, tokens, parent, u_accept, u_draw, *, q=None, n_nodes=None, out=None, status=None, stream=None):
+    """Sampled acceptance along trees from given random numbers: the target's probabilities p [R, T, V] float32 after each node, tokens
+    and parent (None: chains) [R, T] int32, u_accept [R, T] and u_draw [R] float64 in [0, 1); q [R, T, V]: the distributions that
+    each node's children were drawn from (None: they were not drawn). Returns (out_tokens [R, T], n_accepted [R], path [R, T],
+    status) as dspark_tree_accept does."""
+    if stream is not None:
+        return _on(stream, dspark_tree_verify, locals())
+    R, T = tokens.shape
+    V = p.shape[-1]
+    dev = tokens.device
+    if out is None:
+        out = tuple(torch.empty(z, dtype=torch.int32, device=dev) for z in ((R, T), (R,), (R, T)))
+    status = new_status(dev) if status is None else status
+    _check(lib().dspark_tree_verify(_p(p), _rows3(p, R, T, V), _p(q), 0 if q is None else _rows3(q, R, T, V), V, _i32(tokens, R, T),
+                                    _i32(parent, R, T), _i32(n_nodes, R), _f64(u_accept, R, T), _f64(u_draw, R), R, T,
+                                    _i32(out[0], R, T), _i32(out[1], R), _i32(out[2], R, T), _p(status), _stream(stream)),
+           "dspark_tree_verify")
+    return tuple(out) + (status,)

@@ -82,6 +82,7 @@ extern "C" size_t dspark_workspace_size(dspark_op op, int64_t R, int32_t B, int6
     case DSPARK_OP_LATTICE_ROW:
       return dspark_internal_ws_lattice_row(R, B, V);
     case DSPARK_OP_TREE_ATTENTION:
+    case DSPARK_OP_TREE_ATTENTION_Q8:
       return dspark_internal_ws_tree_attention(R, B, V, K);
     default:
       return 0;

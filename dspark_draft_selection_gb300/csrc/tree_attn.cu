@@ -30,8 +30,6 @@
 
 #include "tree_attn.cuh"
 
-extern "C" size_t dspark_internal_ws_tree_attention(int64_t R, int32_t T, int64_t cols, int32_t heads);
-
 namespace {
 
 constexpr int TA_KT = 128;                 // keys per tile
@@ -940,6 +938,8 @@ cudaError_t ta_dispatch_tc(const TaArgs& a, int grid, const CUtensorMap& k, cons
   return a.softcap > 0.0f ? ta_launch_tc<DP, false, true>(a, grid, k, v, st) : ta_launch_tc<DP, false, false>(a, grid, k, v, st);
 }
 
+}  // namespace
+
 void ta_tanh_coefficients(TaArgs& a, float scale, float cap) {
   static const double p[7] = {0x1.fffffep-1, -0x1.55540ap-2, 0x1.10e672p-3, -0x1.b5eb8p-5, 0x1.4c6e4ap-6, -0x1.968b3ap-8, 0x1.10e592p-10};
   static const double q[4] = {0x1.fffffep-1, -0x1.5551c6p-2, 0x1.10110cp-3, -0x1.8b7242p-5};
@@ -963,9 +963,12 @@ void ta_tanh_coefficients(TaArgs& a, float scale, float cap) {
   a.narrow_to = scaled(q, 4, 0.375f, [&](int k, float x) { a.narrow[k] = make_float2(x, x); });
 }
 
-constexpr size_t TA_WS_PREF = 4352;        // pref[TA_MAXR + 1], rounded up to 256 bytes
-
-}  // namespace
+cudaError_t ta_launch_join(const TaArgs& a, dspark_dtype dtype, int grid, int64_t jobs, cudaStream_t st) {
+  const dim3 jg{unsigned(ds_ceil_div(jobs, 8))}, jb{256};
+  auto go = [&](auto kern) { return ds_launch(kern, jg, jb, 0, st, a, uint32_t(grid), jobs); };
+  if (dtype == DSPARK_BF16) return a.c.head_dim <= 128 ? go(tree_attn_join_kernel<__nv_bfloat16, 1>) : go(tree_attn_join_kernel<__nv_bfloat16, 2>);
+  return a.c.head_dim <= 128 ? go(tree_attn_join_kernel<float, 1>) : go(tree_attn_join_kernel<float, 2>);
+}
 
 // Partial results of 2 slots per block: rs rows x (head_dim sums + reference and sums). rs * head_dim is at
 // most the group's T * cols / heads, and at most 256 rows of 256 columns (one block per SM) or 64 rows of
@@ -1033,13 +1036,6 @@ extern "C" dspark_status dspark_tree_attention(const void* q, int64_t ldq, int64
   // 64 columns have their own form: 64 rows 54.6 us, 512 rows 167 us, padded to 128 columns 60.5 and 183 us.
   if (maps) DS_CUDA_TRY(D <= 64 ? ta_dispatch_tc<64>(a, grid, mk, mv, stream) : ta_dispatch_tc<128>(a, grid, mk, mv, stream));
   else DS_CUDA_TRY(ta_launch_float(a, grid, stream));
-  const dim3 jg{unsigned(ds_ceil_div(jobs, 8))}, jb{256};
-  if (cache->dtype == DSPARK_BF16) {
-    if (D <= 128) DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<__nv_bfloat16, 1>, jg, jb, 0, stream, a, uint32_t(grid), jobs));
-    else DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<__nv_bfloat16, 2>, jg, jb, 0, stream, a, uint32_t(grid), jobs));
-  } else {
-    if (D <= 128) DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<float, 1>, jg, jb, 0, stream, a, uint32_t(grid), jobs));
-    else DS_CUDA_TRY(ds_launch(tree_attn_join_kernel<float, 2>, jg, jb, 0, stream, a, uint32_t(grid), jobs));
-  }
+  DS_CUDA_TRY(ta_launch_join(a, cache->dtype, grid, jobs, stream));
   return DSPARK_OK;
 }

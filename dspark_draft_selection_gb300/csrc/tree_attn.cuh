@@ -8,6 +8,13 @@
 constexpr int TA_MAXR = 1024;
 constexpr int TA_MAXT = 512;
 
+// A cache in 8 bits: what TaArgs::c, whose strides are then bytes and whose dtype is the queries', does not say.
+struct TaQ8 {
+  const uint8_t *k_scale, *v_scale;
+  int64_t page_stride, token_stride, head_stride;   // of the scales
+  int32_t e4m3, vec8;          // vec8: rows of codes start on 8-byte boundaries
+};
+
 struct TaArgs {
   const void* q;
   int64_t ldq;
@@ -32,6 +39,7 @@ struct TaArgs {
   float* part_o;               // [slots][rs][D] sums of weights times values, relative to the maximum
   int32_t* status;
   uint32_t first_wait;
+  TaQ8 q8;
 };
 
 // The work is a line of tiles: requests in order, in each its (key head, row group) items in order,
@@ -202,6 +210,20 @@ DS_DEV int64_t ta_slot(const TaArgs& a, int r, int64_t s) {
   return int64_t(p) * a.c.page_stride + (s - e * a.c.page_size) * a.c.token_stride;
 }
 
+// The same of a cache in 8 bits; `scale`: the slot's offset among the scales.
+DS_DEV int64_t ta_slot_q8(const TaArgs& a, int r, int64_t s, int64_t& scale) {
+  const int64_t e = s / a.c.page_size;
+  if (e >= a.c.table_pages) return -1;
+  const int32_t p = a.c.page_table[int64_t(r) * a.c.ld_table + e];
+  if (p < 0 || p >= a.c.num_pages) {
+    ds_set_error(a.status, DSPARK_ERANGE);
+    return -1;
+  }
+  const int64_t t = s - e * a.c.page_size;
+  scale = int64_t(p) * a.q8.page_stride + t * a.q8.token_stride;
+  return int64_t(p) * a.c.page_stride + t * a.c.token_stride;
+}
+
 DS_DEV float ta_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -218,5 +240,11 @@ DS_DEV float ta_tanh(float x2, float cap) {
 constexpr float TA_LOG2E = 1.4426950408889634f;
 constexpr float TA_LN2 = 0.6931471805599453f;
 
-// Join of the partial results and the launch of it (tree_attn.cu).
+// The kernels in float32 arithmetic (tree_attn_float.cu, tree_attn_q8_float.cu), the coefficients of the cap's polynomials and the
+// join of the partial results (tree_attn.cu; `dtype` of the result).
 cudaError_t ta_launch_float(const TaArgs& a, int grid, cudaStream_t st);
+cudaError_t ta_launch_float_q8(const TaArgs& a, int grid, cudaStream_t st);
+void ta_tanh_coefficients(TaArgs& a, float scale, float cap);
+cudaError_t ta_launch_join(const TaArgs& a, dspark_dtype dtype, int grid, int64_t jobs, cudaStream_t st);
+constexpr size_t TA_WS_PREF = 4352;        // pref[TA_MAXR + 1], rounded up to 256 bytes
+extern "C" size_t dspark_internal_ws_tree_attention(int64_t R, int32_t T, int64_t cols, int32_t heads);

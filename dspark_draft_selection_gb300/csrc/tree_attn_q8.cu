@@ -1,0 +1,53 @@
+// tree_attn_q8.cu - attention of drafted nodes, or of one new token, over a paged key/value cache in 8 bits
+// (dspark_tree_attention_q8): the entry point.
+//
+// openvino.genai PR #4847, Fixes > Split validation windows, and optimum-intel PR #2098 (paged attention targets): the target's
+// pass over the drafted candidates of several requests at once.
+#include "cache_q8.cuh"
+#include "tree_attn.cuh"
+
+extern "C" dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, dspark_dtype dtype, int64_t R, int32_t T, int32_t Hq,
+                                                  const dspark_qcache* cache, const int32_t* ctx_len, const int32_t* n_nodes,
+                                                  const uint32_t* mask, float scale, float softcap, void* out, int64_t ldo,
+                                                  float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                                  dspark_stream_t stream) {
+  DS_REQUIRE(ds_dtype_ok(dtype) && q8_cache_ok(cache, false) && R >= 0 && R <= TA_MAXR && T >= 1 && T <= TA_MAXT);
+  DS_REQUIRE(Hq >= 1 && Hq <= 1024 && Hq % cache->heads == 0);
+  const int64_t D = cache->head_dim;
+  DS_REQUIRE(ldq >= Hq * D && ldo >= Hq * D && scale > 0.0f && scale < INFINITY && softcap >= 0.0f && softcap < INFINITY);
+  if (R == 0) return DSPARK_OK;
+  const size_t e = size_t(ds_dtype_size(dtype));
+  DS_REQUIRE(q && ctx_len && out && dev_status && ds_aligned(q, e) && ds_aligned(out, e));
+  if (!ws || !ds_aligned(ws, 256) || ws_bytes < dspark_internal_ws_tree_attention(R, T, Hq * D, cache->heads))
+    return DSPARK_EWORKSPACE;
+  TaArgs a{};
+  a.q = q; a.ldq = ldq; a.out = out; a.ldo = ldo; a.lse = lse; a.ctx_len = ctx_len; a.n_nodes = n_nodes; a.mask = mask;
+  a.R = int32_t(R); a.T = T; a.Hq = Hq; a.G = Hq / cache->heads; a.W = (T + 31) / 32;
+  a.c.k = cache->k; a.c.v = cache->v; a.c.dtype = dtype; a.c.n_layers = 1;
+  a.c.page_stride = cache->page_stride; a.c.token_stride = cache->token_stride; a.c.head_stride = cache->head_stride;
+  a.c.num_pages = cache->num_pages; a.c.page_size = cache->page_size; a.c.heads = cache->heads; a.c.head_dim = cache->head_dim;
+  a.c.page_table = cache->page_table; a.c.ld_table = cache->ld_table; a.c.table_pages = cache->table_pages;
+  dspark_qcache one = *cache;
+  one.layer_stride = 0;
+  a.q8 = TaQ8{cache->k_scale, cache->v_scale, cache->scale_page_stride, cache->scale_token_stride, cache->scale_head_stride,
+              cache->code == DSPARK_E4M3, q8_codes_aligned(&one, 8)};
+  ta_tanh_coefficients(a, scale, softcap);
+  a.rows = T * a.G; a.scale = scale; a.softcap = softcap; a.status = dev_status; a.first_wait = g_ds_first_wait_polls.load();
+  a.kt = 64;
+  // the running tile count of all requests is 32 bits wide (lengths are cut to what the table holds)
+  DS_REQUIRE(R * ds_ceil_div(std::min<int64_t>(int64_t(cache->table_pages) * cache->page_size, int64_t(INT32_MAX)) + TA_MAXT, a.kt) <= INT32_MAX);
+  const int64_t groups = ds_ceil_div(a.rows, 64);    // groups of 64 rows or fewer, as even as sixteens allow
+  a.rpg = int32_t(ds_ceil_div(a.rows, groups * 16) * 16);
+  a.mg = int32_t(ds_ceil_div(a.rows, a.rpg));
+  a.rs = std::min(a.rows, a.rpg);
+  const int64_t jobs = R * cache->heads * int64_t(a.mg) * a.rs;         // rows of all items
+  DS_REQUIRE(jobs <= INT32_MAX);
+  const int grid = ds_num_sms() * (D > 128 ? 1 : 2);
+  uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+  a.pref = reinterpret_cast<int32_t*>(w);
+  a.part_o = reinterpret_cast<float*>(w + TA_WS_PREF);
+  a.part_ml = reinterpret_cast<float4*>(a.part_o + 2 * int64_t(grid) * a.rs * D);
+  DS_CUDA_TRY(ta_launch_float_q8(a, grid, stream));
+  DS_CUDA_TRY(ta_launch_join(a, dtype, grid, jobs, stream));
+  return DSPARK_OK;
+}

@@ -83,7 +83,8 @@ typedef enum {
   DSPARK_OP_VERIFY = 5,
   DSPARK_OP_D2T_CHECK = 6,
   DSPARK_OP_LATTICE_ROW = 7,
-  DSPARK_OP_TREE_ATTENTION = 8
+  DSPARK_OP_TREE_ATTENTION = 8,
+  DSPARK_OP_TREE_ATTENTION_Q8 = 9
 } dspark_op;
 
 /*
@@ -513,6 +514,115 @@ dspark_status dspark_tree_accept(const int32_t* tokens, const int32_t* parent, c
 dspark_status dspark_cache_commit(const dspark_kvcache* cache, const int32_t* ctx_len,
                                   const int32_t* path, const int32_t* n_accepted, int64_t R, int32_t T,
                                   int32_t* new_len, int32_t* dev_status, dspark_stream_t stream);
+
+/*
+ * The same step over a cache kept in 8 bits.
+ *
+ * A column of a key or value is a code of one byte; each block of 32 columns of a head (columns 32 b .. 32 b + 31, the last
+ * one as far as head_dim goes) shares a power of two, kept as one scale byte: the column is code * 2^(byte - 127). Codes are
+ * DSPARK_E4M3 (8-bit floating point, 4 exponent and 3 fraction bits, largest 448; 0x7F and 0xFF, which that format leaves to what is not
+ * a number, stand for 480 and -480 here and are never written) or DSPARK_INT8 (-127..127; -128 is read as such and never
+ * written). Bytes 1..245 are written; 0 is read as 1 and more than 245 as 245, so that every column is a finite number, which
+ * bf16 and float32 hold exactly. (From byte 127 - 117 on; a column whose value is below 2^-126 may be read as 0.)
+ *
+ * Quantisation, in float32, of a block's numbers y: m = the largest |y| that is finite, e = the least whole number from -126 to 118 with
+ * m <= 448 * 2^e (E4M3) or 127 * 2^e (INT8), byte = e + 127, code = y * 2^-e rounded to the nearest code, ties to even. Magnitudes past the
+ * largest code (m > 448 * 2^118) become that code. An infinity becomes the largest code of its sign and what is not a number code 0;
+ * either sets DSPARK_ENONFINITE on *dev_status.
+ *
+ * Codes are two buffers (keys, values) of one layout, scales two more of one layout: the code of (layer l, page p, place t, head h,
+ * column d) lies at l * layer_stride + p * page_stride + t * token_stride + h * head_stride + d, the scale of block b at
+ * l * scale_layer_stride + p * scale_page_stride + t * scale_token_stride + h * scale_head_stride + b (bytes; strides >= 0). A
+ * layout whose slots' scales lie side by side for a head (scale_token_stride = (head_dim + 31) / 32) is read in the fewest sectors.
+ * Pages, slots, n_nodes and ctx_len are those of dspark_kvcache, and so is what happens to slots and pages out of range.
+ */
+typedef enum { DSPARK_E4M3 = 0, DSPARK_INT8 = 1 } dspark_code;
+
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  dspark_code code;
+  int32_t n_layers; /* dspark_cache_commit_q8 treats every layer; the others use the first */
+  int64_t layer_stride, page_stride, token_stride, head_stride;
+  int64_t scale_layer_stride, scale_page_stride, scale_token_stride, scale_head_stride;
+  int64_t num_pages;
+  int32_t page_size, heads, head_dim;
+  const int32_t* page_table;
+  int32_t ld_table, table_pages;
+} dspark_qcache;
+
+/*
+ * dspark_rope_append for a cache in 8 bits: q, k, v and q_out are of `dtype`, the other arguments as there. Here every product and
+ * every sum of a rotation is rounded to float32 by itself (x1 c - x2 s, x2 c + x1 s), for queries and keys, so that the codes do not
+ * depend on how a program contracts them; queries are then rounded to `dtype`, keys (as float32) and values are quantised.
+ */
+dspark_status dspark_rope_append_q8(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                    const void* v, int64_t ldv, dspark_dtype dtype, int64_t R, int32_t T,
+                                    int32_t Hq, const int32_t* pos, int32_t A, const float* cos_sin,
+                                    int64_t P, int32_t rot, const int32_t* axis, int32_t interleaved,
+                                    const dspark_qcache* cache, const int32_t* ctx_len,
+                                    const int32_t* n_nodes, void* q_out, int64_t ldo,
+                                    int32_t* dev_status, dspark_stream_t stream);
+
+/*
+ * dspark_tree_attention over a cache in 8 bits: q and out are of `dtype`, the other arguments, the definition and the limits as
+ * there, k and v being the numbers that the codes stand for. T = 1 without a mask is the attention of one new token. With bf16
+ * queries the products run on the tensor cores and the weights p are rounded to bf16 for the product with v (head_dim a multiple of 16 up to
+ * 128, page_size % 8 == 0, 16-byte aligned rows of codes, strides above 0; others in float32). ws: dspark_workspace_size(DSPARK_OP_TREE_ATTENTION_Q8, R, T,
+ * Hq * head_dim, heads) bytes.
+ */
+dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, dspark_dtype dtype, int64_t R,
+                                       int32_t T, int32_t Hq, const dspark_qcache* cache,
+                                       const int32_t* ctx_len, const int32_t* n_nodes,
+                                       const uint32_t* mask, float scale, float softcap, void* out,
+                                       int64_t ldo, float* lse, void* ws, size_t ws_bytes,
+                                       int32_t* dev_status, dspark_stream_t stream);
+
+/*
+ * dspark_cache_commit for a cache in 8 bits: codes and scales move, the numbers stay what they were.
+ */
+dspark_status dspark_cache_commit_q8(const dspark_qcache* cache, const int32_t* ctx_len,
+                                     const int32_t* path, const int32_t* n_accepted, int64_t R, int32_t T,
+                                     int32_t* new_len, int32_t* dev_status, dspark_stream_t stream);
+
+/*
+ * Reads a cache in 8 bits back: row (r, i) = r * S + i of k_out and v_out [R * S, ld] (`dtype`, the cache's heads side by side)
+ * becomes the key and value of slot start[r] + i of request r, for i < n[r] (start [R] int32 device, NULL: 0; n [R] int32 device).
+ * Rows i >= n[r] are left as they were. n[r] outside 0..S or start[r] < 0 sets DSPARK_EINVAL on *dev_status and reads nothing for
+ * that request; a slot past the page table's row or a page id out of range sets DSPARK_ERANGE and gives zeros. k_out and v_out
+ * may not overlap.
+ */
+dspark_status dspark_cache_read_q8(const dspark_qcache* cache, const int32_t* start, const int32_t* n,
+                                   int64_t R, int32_t S, dspark_dtype dtype, void* k_out, void* v_out,
+                                   int64_t ld, int32_t* dev_status, dspark_stream_t stream);
+
+/*
+ * Sampled acceptance along a tree from given random numbers (dspark_verify does it for chains from logits and seeds).
+ * p: [R * T, ldp] float32 device, V columns: row r * T + i is the target's distribution after node i (with whatever filters the
+ * caller applies; its entries are finite and >= 0 and sum to 1). q: NULL, or rows of the same form ([R * T, ldq]): row r * T + i is the
+ * distribution that node i's children were drawn from, independently of each other. NULL: the children were not drawn (the best
+ * candidates, say) and count as certain. tokens, parent (NULL: chains), n_nodes as in dspark_tree_accept; u_accept [R, T] and u_draw [R]
+ * float64 device, in [0, 1).
+ * From node 0 on, the children x_1, x_2, .. of the node the walk is on are tested in the order of their numbers against the residual
+ * rho = max(0, p - a q) / b, with a = 0 and b = 1 at first:
+ *   accepted when u_accept[x] b q(x) < max(0, p(x) - a q(x)); the walk goes on from x;
+ *   else a becomes a + b, and b the sum over the vocabulary of max(0, p - a q) with that a.
+ * (That is rejection sampling from p with one draw after the other: rho becomes max(0, rho - q), normalised.) Without q, x is
+ * accepted when u_accept[x] m < p(x), m = 1 at first; else m becomes m - p(x), and p(x) counts as 0 from then on at this node.
+ * Where no child is accepted the last token is drawn from the residual: the first id, in ascending order, at which the running sum of max(0, p - a q)
+ * (or of p without the refused tokens) passes u_draw[r] times its total; if rounding leaves none, the last id whose term is above 0. A residual
+ * without mass is replaced by p. Sums, a, b and m are float64 or pairs of float32 (48 bits).
+ * Outputs as dspark_tree_accept writes them: out_tokens [R, T] (the accepted tokens, the drawn one, then -1), n_accepted [R], path
+ * [R, T]. A token outside 0..V - 1 of a tested node sets DSPARK_ERANGE on *dev_status and is refused with nothing else changed; a row whose sum is not finite or not
+ * above 0 sets DSPARK_ENONFINITE and draws -1. Node 0's token is not looked at. n_r = 0 gives n_accepted = -1 and -1 everywhere. T 1..512, V 1..2^30.
+ */
+dspark_status dspark_tree_verify(const float* p, int64_t ldp, const float* q, int64_t ldq, int64_t V,
+                                 const int32_t* tokens, const int32_t* parent, const int32_t* n_nodes,
+                                 const double* u_accept, const double* u_draw, int64_t R, int32_t T,
+                                 int32_t* out_tokens, int32_t* n_accepted, int32_t* path,
+                                 int32_t* dev_status, dspark_stream_t stream);
 
 /*
  * Failure-detection test hook (not part of the method): sets the poll limit of the first wait
