@@ -12,7 +12,7 @@ constexpr int TA_MAXT = 512;
 struct TaQ8 {
   const uint8_t *k_scale, *v_scale;
   int64_t page_stride, token_stride, head_stride;   // of the scales
-  int32_t e4m3, vec8;          // vec8: rows of codes start on 8-byte boundaries
+  int32_t e4m3, vec8, vec4;    // rows of codes start on 8-byte boundaries, of scales on 4-byte ones
 };
 
 struct TaArgs {
@@ -244,6 +244,7 @@ constexpr float TA_LN2 = 0.6931471805599453f;
 // join of the partial results (tree_attn.cu; `dtype` of the result).
 cudaError_t ta_launch_float(const TaArgs& a, int grid, cudaStream_t st);
 cudaError_t ta_launch_float_q8(const TaArgs& a, int grid, cudaStream_t st);
+cudaError_t ta_launch_q8_rows(const TaArgs& a, int grid, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st);   // tree_attn_q8_rows.cu
 void ta_tanh_coefficients(TaArgs& a, float scale, float cap);
 cudaError_t ta_launch_join(const TaArgs& a, dspark_dtype dtype, int grid, int64_t jobs, cudaStream_t st);
 constexpr size_t TA_WS_PREF = 4352;        // pref[TA_MAXR + 1], rounded up to 256 bytes

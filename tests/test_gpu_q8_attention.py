@@ -189,10 +189,11 @@ def test_pages_and_lengths_out_of_range(T):
                          ([64, cap, 64], [T, T, T], ERANGE), ([64, 2 ** 31 - 1, 64], [T, T, T], ERANGE)):
         out, lse, st = ds.dspark_tree_attention_q8(c.q, c.cache, c.table, torch.tensor(ctx, dtype=torch.int32, device="cuda"),
                                                    n_nodes=torch.tensor(n, dtype=torch.int32, device="cuda"), scale=c.scale)
-        assert ds.read_status(st) == code
-        assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
-        if code == EINVAL or ctx[1] != 64:
-            assert not out[1].any() and torch.isneginf(lse[1]).all()
+        # the other requests' results (the work is split otherwise, so not to the bit), and zeros for this one
+        c.out, c.lse, c.status = out, lse, st
+        c.ctx, c.n = [64, 0, 64], [T, 0, T]
+        c.check(status=code)
+        c.ctx, c.n = [64] * 3, [T] * 3
 
 
 @pytest.mark.parametrize("T", [1, 7, 40])
