@@ -65,6 +65,7 @@ extern "C" size_t dspark_internal_ws_verify(int64_t R, int32_t B, int64_t V);
 extern "C" size_t dspark_internal_ws_lattice_row(int64_t R, int32_t B, int64_t V);
 
 extern "C" size_t dspark_internal_ws_tree_attention(int64_t R, int32_t T, int64_t cols, int32_t heads);
+extern "C" size_t dspark_internal_ws_tree_attention_q8(int64_t R, int32_t T, int64_t cols, int32_t heads);
 
 extern "C" size_t dspark_workspace_size(dspark_op op, int64_t R, int32_t B, int64_t V, int32_t K) {
   if (R < 0 || B < 0 || V < 0) return 0;
@@ -82,8 +83,9 @@ extern "C" size_t dspark_workspace_size(dspark_op op, int64_t R, int32_t B, int6
     case DSPARK_OP_LATTICE_ROW:
       return dspark_internal_ws_lattice_row(R, B, V);
     case DSPARK_OP_TREE_ATTENTION:
-    case DSPARK_OP_TREE_ATTENTION_Q8:
       return dspark_internal_ws_tree_attention(R, B, V, K);
+    case DSPARK_OP_TREE_ATTENTION_Q8:
+      return dspark_internal_ws_tree_attention_q8(R, B, V, K);
     default:
       return 0;
   }

@@ -37,6 +37,7 @@ struct TaArgs {
   int32_t* pref;               // [R + 1] running sum of the requests' tile counts
   float4* part_ml;             // [slots][rs] (reference in log2 units, sum of the weights, sum the result is divided by)
   float* part_o;               // [slots][rs][D] sums of weights times values, relative to the maximum
+  float* warp_o;               // [blocks][warps][rs][D] the same of single warps (tree_attn_q8_rows.cu)
   int32_t* status;
   uint32_t first_wait;
   TaQ8 q8;
@@ -249,3 +250,4 @@ void ta_tanh_coefficients(TaArgs& a, float scale, float cap);
 cudaError_t ta_launch_join(const TaArgs& a, dspark_dtype dtype, int grid, int64_t jobs, cudaStream_t st);
 constexpr size_t TA_WS_PREF = 4352;        // pref[TA_MAXR + 1], rounded up to 256 bytes
 extern "C" size_t dspark_internal_ws_tree_attention(int64_t R, int32_t T, int64_t cols, int32_t heads);
+extern "C" size_t dspark_internal_ws_tree_attention_q8(int64_t R, int32_t T, int64_t cols, int32_t heads);

@@ -23,6 +23,15 @@ bool tq_tensor_map(CUtensorMap* m, void* base, const dspark_qcache& c, int cols,
 
 }  // namespace
 
+// The partial results of dspark_tree_attention, and of each warp of the kernel for few rows one more of at most 16 (16 warps) or 32
+// rows (8 warps) of 128 columns.
+extern "C" size_t dspark_internal_ws_tree_attention_q8(int64_t R, int32_t T, int64_t cols, int32_t heads) {
+  const size_t base = dspark_internal_ws_tree_attention(R, T, cols, heads);
+  if (!base) return 0;
+  const int64_t item = int64_t(T) * (cols / heads), warps = 16 * int64_t(ds_num_sms()) * std::min<int64_t>(item, 16 * 128);
+  return base + size_t(ds_ceil_div(warps * 4, 256) * 256);
+}
+
 extern "C" dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, dspark_dtype dtype, int64_t R, int32_t T, int32_t Hq,
                                                   const dspark_qcache* cache, const int32_t* ctx_len, const int32_t* n_nodes,
                                                   const uint32_t* mask, float scale, float softcap, void* out, int64_t ldo,
@@ -35,7 +44,7 @@ extern "C" dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, ds
   if (R == 0) return DSPARK_OK;
   const size_t e = size_t(ds_dtype_size(dtype));
   DS_REQUIRE(q && ctx_len && out && dev_status && ds_aligned(q, e) && ds_aligned(out, e));
-  if (!ws || !ds_aligned(ws, 256) || ws_bytes < dspark_internal_ws_tree_attention(R, T, Hq * D, cache->heads))
+  if (!ws || !ds_aligned(ws, 256) || ws_bytes < dspark_internal_ws_tree_attention_q8(R, T, Hq * D, cache->heads))
     return DSPARK_EWORKSPACE;
   TaArgs a{};
   a.q = q; a.ldq = ldq; a.out = out; a.ldo = ldo; a.lse = lse; a.ctx_len = ctx_len; a.n_nodes = n_nodes; a.mask = mask;
@@ -67,7 +76,7 @@ extern "C" dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, ds
   a.box = box;
   if (maps) {
     a.kt = 16;
-    a.rpg = a.rows <= 16 ? 16 : 32;
+    a.rpg = a.rows <= 8 ? 8 : a.rows <= 16 ? 16 : 32;
   } else {
     a.kt = 64;
     const int64_t groups = ds_ceil_div(a.rows, 64);  // groups of 64 rows or fewer, as even as sixteens allow
@@ -82,6 +91,7 @@ extern "C" dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, ds
   a.pref = reinterpret_cast<int32_t*>(w);
   a.part_o = reinterpret_cast<float*>(w + TA_WS_PREF);
   a.part_ml = reinterpret_cast<float4*>(a.part_o + 2 * int64_t(grid) * a.rs * D);
+  a.warp_o = reinterpret_cast<float*>(w + dspark_internal_ws_tree_attention(R, T, Hq * D, cache->heads));
   DS_CUDA_TRY(maps ? ta_launch_q8_rows(a, grid, mk, mv, stream) : ta_launch_float_q8(a, grid, stream));
   DS_CUDA_TRY(ta_launch_join(a, dtype, grid, jobs, stream));
   return DSPARK_OK;

@@ -520,10 +520,10 @@ dspark_status dspark_cache_commit(const dspark_kvcache* cache, const int32_t* ct
  *
  * A column of a key or value is a code of one byte; each block of 32 columns of a head (columns 32 b .. 32 b + 31, the last
  * one as far as head_dim goes) shares a power of two, kept as one scale byte: the column is code * 2^(byte - 127). Codes are
- * DSPARK_E4M3 (8-bit floating point, 4 exponent and 3 fraction bits, largest 448; 0x7F and 0xFF, which that format leaves to what is not
- * a number, stand for 480 and -480 here and are never written) or DSPARK_INT8 (-127..127; -128 is read as such and never
- * written). Bytes 1..245 are written; 0 is read as 1 and more than 245 as 245, so that every column is a finite number, which
- * bf16 and float32 hold exactly. (From byte 127 - 117 on; a column whose value is below 2^-126 may be read as 0.)
+ * DSPARK_E4M3 (8-bit floating point, 4 exponent and 3 fraction bits, largest 448; 0x7F and 0xFF, which that format leaves to what is
+ * not a number, are never written: what a read of one, or a row that sees one, gives is not defined, and a row that does not see it is not
+ * affected) or DSPARK_INT8 (-127..127; -128 is read as such and never written). Bytes 1..245 are written; 0 is read as 1 and more than
+ * 245 as 245, so that every column is a finite number, which bf16 and float32 hold exactly (one below 2^-126 may be read as 0).
  *
  * Quantisation, in float32, of a block's numbers y: m = the largest |y| that is finite, e = the least whole number from -126 to 118 with
  * m <= 448 * 2^e (E4M3) or 127 * 2^e (INT8), byte = e + 127, code = y * 2^-e rounded to the nearest code, ties to even. Magnitudes past the

@@ -5,7 +5,7 @@ the format is that of dspark.h: blocks of 32 columns share a power of two, codes
 """
 import numpy as np
 
-# the numbers of e4m3's codes 0..127, from the format: 4 exponent bits (bias 7), 3 fraction bits, no infinities (0x7F reads as 480)
+# the numbers of e4m3's codes 0..127, from the format: 4 exponent bits (bias 7), 3 fraction bits, no infinities (0x7F is no number; 480 here)
 E4M3 = np.array([(c & 7) / 8 * 2.0 ** -6 if c < 8 else (1 + (c & 7) / 8) * 2.0 ** ((c >> 3) - 7) for c in range(128)])
 
 

@@ -36,7 +36,10 @@ def paged(gen, R, slots, page, H, D, code, layers=None, order="phtd", sorder="ph
         t = buf.cuda()[off:].view(shape).permute([order.index(x) for x in "lpthd"])
         return t if layers else t[0]
 
-    codes = lambda n: torch.randint(0, 256, (n,), generator=gen).to(torch.uint8)  # noqa: E731
+    def codes(n):                                            # (0x7F and 0xFF are no numbers in e4m3)
+        c = torch.randint(0, 256, (n,), generator=gen).to(torch.uint8)
+        return torch.where((c & 127) == 127, c - 1, c) if code == "e4m3" else c
+
     bytes_ = lambda n: torch.randint(low, high + 1, (n,), generator=gen).to(torch.uint8)  # noqa: E731
     k, v = (make(D, order, codes, offset).view(CODES[code]) for _ in range(2))
     ks, vs = (make((D + 31) // 32, sorder, bytes_, 0) for _ in range(2))
