@@ -246,6 +246,7 @@ constexpr float TA_LN2 = 0.6931471805599453f;
 cudaError_t ta_launch_float(const TaArgs& a, int grid, cudaStream_t st);
 cudaError_t ta_launch_float_q8(const TaArgs& a, int grid, cudaStream_t st);
 cudaError_t ta_launch_q8_rows(const TaArgs& a, int grid, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st);   // tree_attn_q8_rows.cu
+cudaError_t ta_launch_q8_tc(const TaArgs& a, int grid, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st);     // tree_attn_q8_tc.cu
 void ta_tanh_coefficients(TaArgs& a, float scale, float cap);
 cudaError_t ta_launch_join(const TaArgs& a, dspark_dtype dtype, int grid, int64_t jobs, cudaStream_t st);
 constexpr size_t TA_WS_PREF = 4352;        // pref[TA_MAXR + 1], rounded up to 256 bytes

@@ -17,18 +17,18 @@ bool tq_tensor_map(CUtensorMap* m, void* base, const dspark_qcache& c, int cols,
   const cuuint32_t bx[4] = {cuuint32_t(cols), cuuint32_t(box), 1, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            cols == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
-// The partial results of dspark_tree_attention, and of each warp of the kernel for few rows one more of at most 16 (16 warps) or 32
-// rows (8 warps) of 128 columns.
+// The partial results of dspark_tree_attention, and of each warp of the kernel for few rows one more of at most 32 rows of 128 columns.
 extern "C" size_t dspark_internal_ws_tree_attention_q8(int64_t R, int32_t T, int64_t cols, int32_t heads) {
   const size_t base = dspark_internal_ws_tree_attention(R, T, cols, heads);
   if (!base) return 0;
-  const int64_t item = int64_t(T) * (cols / heads), warps = 16 * int64_t(ds_num_sms()) * std::min<int64_t>(item, 16 * 128);
+  const int64_t warps = 12 * int64_t(ds_num_sms()) * std::min<int64_t>(int64_t(T) * (cols / heads), 32 * 128);
   return base + size_t(ds_ceil_div(warps * 4, 256) * 256);
 }
 
@@ -64,19 +64,24 @@ extern "C" dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, ds
     return R * ds_ceil_div(std::min<int64_t>(int64_t(cache->table_pages) * cache->page_size, int64_t(INT32_MAX)) + TA_MAXT, kt) <= INT32_MAX;
   };
   DS_REQUIRE(counts(64));
-  int box = 16;
+  // Few rows a key head: the kernel that widens codes in operand registers; more: the one that stages them for tcgen05.
+  const bool few = a.rows <= 32;
+  int box = few ? 16 : 128;
   while (cache->page_size % box) box >>= 1;
   // Tensor cores: rows of codes that TMA can copy and bf16 rows that 16-byte accesses can.
   const bool tc = dtype == DSPARK_BF16 && D <= 128 && D % 16 == 0 && box >= 8 && q8_codes_aligned(&one, 16) && ds_aligned(q, 16) &&
                   ds_aligned(out, 16) && ldq % 8 == 0 && ldo % 8 == 0 && cache->page_stride > 0 && cache->token_stride > 0 &&
-                  cache->head_stride > 0 && counts(16);
+                  cache->head_stride > 0 && counts(16) && cache->scale_page_stride <= INT32_MAX && cache->scale_token_stride <= INT32_MAX;
   CUtensorMap mk, mv;
   const int cols = D <= 64 ? 64 : 128;
   const bool maps = tc && tq_tensor_map(&mk, cache->k, *cache, cols, box) && tq_tensor_map(&mv, cache->v, *cache, cols, box);
   a.box = box;
-  if (maps) {
+  if (maps && few) {
     a.kt = 16;
     a.rpg = a.rows <= 8 ? 8 : a.rows <= 16 ? 16 : 32;
+  } else if (maps) {
+    a.kt = 128;
+    a.rpg = a.rows > 128 ? 256 : 128;
   } else {
     a.kt = 64;
     const int64_t groups = ds_ceil_div(a.rows, 64);  // groups of 64 rows or fewer, as even as sixteens allow
@@ -92,7 +97,7 @@ extern "C" dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, ds
   a.part_o = reinterpret_cast<float*>(w + TA_WS_PREF);
   a.part_ml = reinterpret_cast<float4*>(a.part_o + 2 * int64_t(grid) * a.rs * D);
   a.warp_o = reinterpret_cast<float*>(w + dspark_internal_ws_tree_attention(R, T, Hq * D, cache->heads));
-  DS_CUDA_TRY(maps ? ta_launch_q8_rows(a, grid, mk, mv, stream) : ta_launch_float_q8(a, grid, stream));
+  DS_CUDA_TRY(!maps ? ta_launch_float_q8(a, grid, stream) : few ? ta_launch_q8_rows(a, grid, mk, mv, stream) : ta_launch_q8_tc(a, grid, mk, mv, stream));
   DS_CUDA_TRY(ta_launch_join(a, dtype, grid, jobs, stream));
   return DSPARK_OK;
 }

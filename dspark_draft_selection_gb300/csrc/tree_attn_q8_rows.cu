@@ -18,7 +18,7 @@
 // bits (2^-12 of a weight; those below 2^-32 of the row's largest to less).
 //
 // Every warp copies its own slices with TMA, NS of them in flight, and waits for nothing but its own barriers. The work is the line of
-// tiles of tree_attn.cuh with 16 keys a tile: a block's share is cut once more into its warps' shares, what two warps leave of an item is joined
+// tiles of tree_attn.cuh with 16 keys a tile: a block's share is cut once more into its warps' shares; what two warps leave of an item is joined
 // at the end in shared memory (in the order of the keys), and what two blocks leave by the join kernel.
 #include <cuda_fp16.h>
 
@@ -36,24 +36,33 @@ constexpr float TQ_NONE = -3e38f;            // reference of a row that has seen
 
 template <int DP, int NQ>
 struct TqLayout {
-  static constexpr int WARPS = NQ == 1 ? 16 : NQ == 2 ? 12 : 8;
+  static constexpr int WARPS = NQ <= 2 ? 12 : 8;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int NS = NQ <= 2 ? 2 : 4;
+  static constexpr int NS = NQ == 1 ? 3 : NQ == 2 ? 2 : 4;
+  static constexpr bool QREG = NQ == 1;                // queries stay in registers
   static constexpr int STEPS = DP / 16;                // contraction steps of K Q^T; row tiles of O^T
   static constexpr uint32_t SLICE = 2 * TQ_KEYS * DP;  // bytes of a slice's keys and values
   // dynamic shared memory: rings of slices (where a warp's last partial result goes when they are done with), scale words, queries
   static constexpr uint32_t RING = NS * SLICE;
   static constexpr uint32_t SCALE = WARPS * RING;      // [WARPS][NS][32] words: scale bytes of 16 keys, then of 16 values
   static constexpr uint32_t QF = SCALE + WARPS * NS * 128;
-  static constexpr uint32_t QW = NQ * STEPS * 256;     // bytes of a warp's queries
+  static constexpr uint32_t QW = QREG ? 0 : NQ * STEPS * 256;   // bytes of a warp's queries
   static constexpr uint32_t TOTAL = QF + WARPS * QW;
   static_assert(8 * NQ * DP * 4 <= RING, "a partial result fits its warp's ring");
 };
 
-DS_DEV void tq_tma_load(uint32_t dst, const void* tmap, int32_t d, int32_t t, int32_t h, int32_t p, uint32_t bar) {
+// A box of keys and the same of values, V bytes behind, by one elected lane of a warp that stays together; BYTES > 0: the arrival that
+// the barrier's phase waits for, with that many bytes to come.
+template <uint32_t V, uint32_t BYTES>
+DS_DEV void tq_tma_pair(uint32_t dst, const void* tk, const void* tv, int32_t t, int32_t h, int32_t p, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(tmap), "r"(d), "r"(t), "r"(h), "r"(p), "r"(bar)
+      "{\n\t.reg .pred e, f;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "setp.ne.and.u32 f, %8, 0, e;\n\t"
+      "@f mbarrier.arrive.expect_tx.shared::cta.b64 _, [%6], %8;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%7, %3, %4, %5}], [%6];\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%9], [%2, {%7, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
+      "l"(tk), "l"(tv), "r"(t), "r"(h), "r"(p), "r"(bar), "r"(0), "n"(BYTES), "r"(dst + V)
       : "memory");
 }
 
@@ -123,8 +132,11 @@ DS_DEV void tq_widen(uint32_t w, const TqFactor& f, uint32_t& first, uint32_t& s
     first = tq_mul2h(a, f.f);
     second = tq_mul2h(b, f.f);
   } else {
-    first = tq_fma2h((w & 0x00FF00FFu) ^ 0x64806480u, f.f, f.c);
-    second = tq_fma2h(((w >> 8) & 0x00FF00FFu) ^ 0x64806480u, f.f, f.c);
+    uint32_t x, y;                                     // (one instruction each, which the compiler makes two of)
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(x) : "r"(w), "r"(0x00FF00FFu), "r"(0x64806480u));
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(y) : "r"(w >> 8), "r"(0x00FF00FFu), "r"(0x64806480u));
+    first = tq_fma2h(x, f.f, f.c);
+    second = tq_fma2h(y, f.f, f.c);
   }
 }
 
@@ -149,17 +161,41 @@ DS_DEV void tq_widen_far(uint32_t w, int elo, int ehi, uint32_t& first, uint32_t
   }
 }
 
-// Largest of each byte over the warp.
-DS_DEV uint32_t tq_max4(uint32_t w) {
-  uint32_t r = 0;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) r |= __reduce_max_sync(0xFFFFFFFFu, (w >> (8 * b)) & 0xFFu) << (8 * b);
-  return r;
-}
+// Of the line of tiles a block has one share, cut once more into its warps' shares. Of an item's nt tiles the block has [a0, a1) and the warp [t0, t1).
+struct TqPiece {
+  int32_t r, hk, g;            // request, key head, row group
+  int32_t a0, a1, nt, t0, t1;
+  DS_DEV bool all() const { return a0 == 0 && a1 == nt; }
+  DS_DEV int64_t slot() const { return 2 * int64_t(blockIdx.x) + (a0 > 0 ? 0 : 1); }
+};
+
+// Walks a warp's share [at, end) of the line.
+struct TqWalk {
+  int64_t at, end;
+  int32_t r;
+  DS_DEV bool find(const TaLens& s, const TaArgs& a, TqPiece& p) {
+    if (at >= end) return false;
+    const int64_t hm = int64_t(a.c.heads) * a.mg;
+    while (s.pref[r + 1] * hm <= at) ++r;
+    const int64_t off = at - s.pref[r] * hm;
+    const int32_t nt = s.pref[r + 1] - s.pref[r], item = int32_t(ta_div(off, uint32_t(nt)));
+    p.r = r;
+    p.nt = nt;
+    p.hk = int32_t(uint32_t(item) / uint32_t(a.mg));
+    p.g = item - p.hk * a.mg;
+    p.t0 = int32_t(off - int64_t(item) * nt);
+    p.t1 = int32_t(min(int64_t(nt), p.t0 + (end - at)));
+    const int64_t i0 = at - p.t0;                      // the item's place on the line
+    p.a0 = int32_t(max(s.at - i0, int64_t(0)));
+    p.a1 = int32_t(min(int64_t(nt), s.end - i0));
+    at += p.t1 - p.t0;
+    return true;
+  }
+};
 
 // A warp's part of an item that it shares with others.
 struct TqPart {
-  TaPiece p;
+  TqPiece p;
   int valid;
 };
 
@@ -173,8 +209,8 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[WARPS][NS];
   __shared__ TaLens s_len;
-  __shared__ TaWalk s_walk[WARPS];
-  __shared__ TaPiece s_piece[WARPS][3];
+  __shared__ TqWalk s_walk[WARPS];
+  __shared__ TqPiece s_piece[WARPS][3];
   __shared__ int s_there[WARPS][3];                    // whether the piece is one
   __shared__ TqPart s_head[WARPS], s_tail[WARPS];      // the first piece, if an earlier warp began it and it ends here; the last, if it goes on
   __shared__ float2 s_ml[2][WARPS][ROWS];              // their references and sums
@@ -185,8 +221,9 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
   uint32_t* scales = reinterpret_cast<uint32_t*>(smem + L::SCALE) + warp * NS * 32;
   uint2* qf = reinterpret_cast<uint2*>(smem + L::QF + warp * L::QW) + lane;
   const int D = a.c.head_dim, nb = q8_blocks(D);
+  const bool narrow = D < DP;                          // some columns are not there
   const bool words = nb == 4 && a.q8.vec4 != 0;        // a slot's scales are one aligned word
-  const TaPiece* piece = s_piece[warp];
+  const TqPiece* piece = s_piece[warp];
   const int* there = s_there[warp];
   ds_pdl_trigger();
   if (lane == 0) {
@@ -206,44 +243,47 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
   };
   if (lane == 0) {
     const int64_t share = s_len.end - s_len.at;
-    TaWalk w;
-    w.init(s_len);
-    w.at = s_len.at + share * warp / WARPS;
-    w.end = s_len.at + share * (warp + 1) / WARPS;
+    TqWalk w;
+    w.at = s_len.at + ta_div(share * warp, WARPS);
+    w.end = s_len.at + ta_div(share * (warp + 1), WARPS);
+    w.r = s_len.r;
     s_walk[warp] = w;
     more(0);
-    more(1);
+    s_there[warp][1] = 0;
   }
   __syncwarp();
   auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
 
   // ---- this warp's slices: the next one to copy, its page known beforehand ----
   int kp = 0;                                          // piece that is worked on
-  int np = 0, nt = piece[0].t0;                        // piece (0: that one, 1: the one after it) and tile of the next copy
+  int np = -1, nt = 0, nt1 = 0;                        // piece (0: that one, 1: the one after it), tile and last tile of the next copy
   bool valid = false;
-  int32_t pg = 0, place = 0;                           // page and place of this lane's key of that slice (lane & 15); pg < 0: no key
+  const uint32_t psize = uint32_t(a.c.page_size);
+  uint32_t key = 0, len = 0, entry = 0, place = 0;     // this lane's key of that slice (lane & 15), the request's keys, the key's page and place
+  int32_t pg = -1, next = -1, hk = 0;                  // that page (-1: no key) and the one after it
+  const int32_t* table = nullptr;
+  const uint8_t* sbase = nullptr;                      // scales of the piece's head: keys' for lanes below 16, else values'
   uint32_t issued = 0, used = 0, pend = 0;
   int pend_at = -1;
-  auto advance = [&]() {                               // finds the next slice and asks for its page
+  auto advance = [&]() {                               // finds the first slice of the next piece that has one
     valid = false;
-    for (;; ++np, nt = piece[(kp + 1) % 3].t0) {
-      if (!there[(kp + np) % 3]) return;
-      if (nt < piece[(kp + np) % 3].t1) break;
-      if (np == 1) return;
+    while (np < 1 && there[(kp + np + 1) % 3]) {
+      ++np;
+      const TqPiece& p = piece[(kp + np) % 3];
+      nt = p.t0;
+      nt1 = p.t1;
+      hk = p.hk;
+      key = uint32_t(nt) * TQ_KEYS + (lane & 15);
+      len = uint32_t(s_len.ctx[p.r]) + uint32_t(s_len.n[p.r]);
+      entry = key / psize;
+      place = key - entry * psize;
+      table = a.c.page_table + int64_t(p.r) * a.c.ld_table;
+      sbase = (lane < 16 ? a.q8.k_scale : a.q8.v_scale) + int64_t(hk) * a.q8.head_stride;
+      pg = key < len ? table[entry] : -1;              // looked at when the slice is copied
+      next = key - place + psize < len ? table[entry + 1] : -1;
+      valid = true;
+      return;
     }
-    const TaPiece& p = piece[(kp + np) % 3];
-    const uint32_t key = uint32_t(nt) * TQ_KEYS + (lane & 15), len = uint32_t(s_len.ctx[p.r]) + uint32_t(s_len.n[p.r]);
-    pg = -1;
-    if (key < len) {
-      const uint32_t e = key / uint32_t(a.c.page_size);
-      place = int32_t(key - e * uint32_t(a.c.page_size));
-      pg = a.c.page_table[int64_t(p.r) * a.c.ld_table + e];
-      if (pg < 0 || pg >= a.c.num_pages) {
-        ds_set_error(a.status, DSPARK_ERANGE);
-        pg = -1;
-      }
-    }
-    valid = true;
   };
   auto flush = [&]() {                                 // the scales asked for last have arrived; no key: 0
     if (pend_at >= 0) scales[pend_at * 32 + lane] = pend;
@@ -251,38 +291,54 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
   };
   auto issue = [&]() {
     flush();
-    const TaPiece& p = piece[(kp + np) % 3];
+    const int32_t seen = pg;
+    const bool there_ = key < len && uint32_t(pg) < uint32_t(a.c.num_pages);
+    if (key < len && !there_) ds_set_error(a.status, DSPARK_ERANGE);
     const int s = int(issued % NS);
+    // boxes of 16 or 8 places, keys' and values', by one lane; past the end, or from a page that does not exist, a box names a page past
+    // the last and reads zeros
+    const int32_t none = int32_t(a.c.num_pages), mine = there_ ? pg : none;
     const uint32_t bar = ds_smem_addr(&s_full[warp][s]), dst = ds_smem_addr(ring + s * L::SLICE);
-    if (lane == 0) ds_mbar_arrive_expect_tx(&s_full[warp][s], L::SLICE);
-    __syncwarp();
-    // boxes of 16 or 8 places: the lane of a box's first key (lanes 16 and above: its values) copies it; past the end, or from a page that
-    // does not exist, a box names a page past the last and reads zeros
-    if ((lane & (a.box - 1)) == 0)
-      tq_tma_load(dst + (lane & 24) * DP, lane < 16 ? &tmK : &tmV, 0, place, p.hk, pg < 0 ? int32_t(a.c.num_pages) : pg, bar);
-    pend = 0;
-    if (pg >= 0) {
-      const uint8_t* at = (lane < 16 ? a.q8.k_scale : a.q8.v_scale) + int64_t(pg) * a.q8.page_stride + int64_t(place) * a.q8.token_stride +
-                          int64_t(p.hk) * a.q8.head_stride;
-      if (words) {
-        pend = *reinterpret_cast<const uint32_t*>(at);
-      } else {
-        for (int b = 0; b < nb; ++b) pend |= uint32_t(at[b]) << (8 * b);
-      }
+    tq_tma_pair<16 * DP, L::SLICE>(dst, &tmK, &tmV, __shfl_sync(0xFFFFFFFFu, int32_t(place), 0), hk, __shfl_sync(0xFFFFFFFFu, mine, 0), bar);
+    if (a.box == 8)
+      tq_tma_pair<16 * DP, 0>(dst + 8 * DP, &tmK, &tmV, __shfl_sync(0xFFFFFFFFu, int32_t(place), 8), hk, __shfl_sync(0xFFFFFFFFu, mine, 8), bar);
+    // scale bytes (strides of scales are below 2^31 here); none: 0
+    const uint8_t* at = sbase + uint64_t(uint32_t(there_ ? pg : 0)) * uint32_t(a.q8.page_stride) + uint64_t(place) * uint32_t(a.q8.token_stride);
+    if (words) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n\tcp.async.commit_group;" ::"r"(ds_smem_addr(scales + s * 32 + lane)), "l"(at),
+                   "r"(there_ ? 4 : 0)
+                   : "memory");
+    } else {
+      pend = 0;
+      for (int b = 0; b < nb; ++b)
+        if (there_) pend |= uint32_t(at[b]) << (8 * b);
+      pend_at = s;
     }
-    pend_at = s;
     ++issued;
-    ++nt;
-    advance();
+    if (++nt < nt1) {
+      key += TQ_KEYS;
+      place += TQ_KEYS;
+      pg = seen;
+      if (place >= psize) {                            // pages of 8 or more places: one or two further
+        do {
+          place -= psize;
+          ++entry;
+          pg = next;
+          next = key - place + psize < len ? table[entry + 1] : -1;
+        } while (place >= psize);
+      }
+    } else {
+      advance();
+    }
   };
   advance();
   const float sc = CAP ? fminf(a.scale * 2.0f * TA_LOG2E / a.softcap, 3e38f) : a.scale * TA_LOG2E;
   const float cap2 = a.softcap * TA_LOG2E, sy = CAP ? a.scale / a.softcap : 0.0f;
   bool ok = true, first = true;
   for (; there[kp % 3]; ++kp) {
-    const TaPiece p = piece[kp % 3];
+    const TqPiece p = piece[kp % 3];
     const int32_t ctx = s_len.ctx[p.r], n = s_len.n[p.r];
-    const int m0 = p.g * a.rpg;
+    const int m0 = p.g * a.rpg, tmask = ctx / TQ_KEYS;   // tiles from tmask on hold nodes or the end of the keys
     if (ok) {
       while (issued - used < NS) {
         if (!valid) advance();
@@ -290,8 +346,18 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
         issue();
       }
     }
+    if (kp == 0) {                                     // the second piece, now that the first's copies are on their way
+      if (lane == 0) more(1);
+      __syncwarp();
+      while (ok && issued - used < NS) {
+        if (!valid) advance();
+        if (!valid) break;
+        issue();
+      }
+    }
     // ---- query rows (n index g of each tile) in the order of the operand registers, in f16 under 2^qe of the row ----
     const __nv_bfloat16* qrow[NQ];
+    uint2 qreg[L::QREG ? STEPS : 1];
     float qfac[NQ][2];                                   // of rows 2 t4, 2 t4 + 1 of each tile: that power back, and the scale
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
@@ -323,8 +389,8 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
         float v[4] = {__uint_as_float(x[st].x << 16), __uint_as_float(x[st].x & 0xFFFF0000u), __uint_as_float(x[st].y << 16), __uint_as_float(x[st].y & 0xFFFF0000u)};
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] *= down;
-        qf[(nq * STEPS + st) * 32] = E4M3 ? make_uint2(tq_pack<false>(v[0], v[1]), tq_pack<false>(v[2], v[3]))
-                                          : make_uint2(tq_pack<false>(v[0], v[2]), tq_pack<false>(v[1], v[3]));
+        (L::QREG ? qreg[L::QREG ? st : 0] : qf[(nq * STEPS + st) * 32]) = E4M3 ? make_uint2(tq_pack<false>(v[0], v[1]), tq_pack<false>(v[2], v[3]))
+                                                                          : make_uint2(tq_pack<false>(v[0], v[2]), tq_pack<false>(v[1], v[3]));
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -340,58 +406,78 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
         mref[nq][e] = TQ_NONE;
         l[nq][e] = 0.0f;
       }
-    uint32_t ev = 0, ek = 0;                           // references: scale bytes of the values' blocks, of keys (all four bytes alike); 0: none
+    // references: scale bytes of the thread's block of values and of keys; `near`: there are some, and no byte in their reach is one that is
+    // read as another
+    uint32_t ev = 0, ek = 0;
+    bool near = false;
     for (int t = p.t0; ok && t < p.t1; ++t) {
       const int s = int(used % NS);
       flush();
       ok = ds_mbar_wait_or_abort(&s_full[warp][s], (used / NS) & 1u, first ? a.first_wait : DS_WAIT_LIMIT, &s_abort);
       ok = __all_sync(0xFFFFFFFFu, ok);
       first = false;
+      if (words) {                                     // a slot's scales: all but the newest NS - 1 copies
+        if (issued - used == NS) asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
       if (!ok) {
         if (!aborted()) ds_set_error(a.status, DSPARK_ETIMEOUT);
         s_abort = 1;
         break;
       }
       const uint8_t *K = ring + s * L::SLICE, *V = K + TQ_KEYS * DP;
-      uint32_t* ws = scales + s * 32;
-      const int64_t nd = int64_t(t) * TQ_KEYS - ctx;
-      // ---- this slice's powers relative to the references: lane k < 16 has key k's four bytes, lane 16 + k its values' ----
-      uint32_t w4 = ws[lane];
-      const bool some = w4 != 0u || nd + (lane & 15) < n;      // a key is there (0 may be its bytes, or a page that is not)
+      const uint8_t *ks = reinterpret_cast<const uint8_t*>(scales + s * 32), *vs = ks + 64;
+      const bool masked = t >= tmask;
+      __syncwarp();                                    // every lane's words are there
+      // ---- this slice's powers relative to the references, as exponents of f16: a thread's two keys (of its columns' block), four values ----
+      uint32_t kb[2], vb[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {                    // bytes 1..245; what is not there is the reference itself
-        const uint32_t x = (w4 >> (8 * b)) & 0xFFu;
-        if (x == 0u || x > uint32_t(Q8_TOP)) w4 = (w4 & ~(0xFFu << (8 * b))) | ((x == 0u ? 1u : uint32_t(Q8_TOP)) << (8 * b));
+      for (int x = 0; x < 2; ++x) kb[x] = ks[(8 * x + g) * 4 + (DP == 128 ? t4 : t4 >> 1)];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) vb[x] = vs[(2 * t4 + (x & 1) + 8 * (x >> 1)) * 4 + (DP == 128 ? g >> 1 : g >> 2)];
+      uint32_t gone = 0;                               // bits 0, 1: keys, 2..5: values that are not there (columns past head_dim, keys past the end)
+      if (narrow) gone = (t4 * (DP / 4) >= D ? 3u : 0u) | (g * (DP / 8) >= D ? 60u : 0u);
+      if (masked) {
+        const int left = int(min(int64_t(ctx) + n - int64_t(t) * TQ_KEYS, int64_t(TQ_KEYS)));
+        gone |= (g >= left ? 1u : 0u) | (8 + g >= left ? 2u : 0u) | (2 * t4 >= left ? 4u : 0u) | (2 * t4 + 1 >= left ? 8u : 0u) |
+                (2 * t4 + 8 >= left ? 16u : 0u) | (2 * t4 + 9 >= left ? 32u : 0u);
       }
-      const int cut = nb < 4 ? 8 * (4 - nb) : 0;
-      const uint32_t used_bytes = 0xFFFFFFFFu >> cut;
-      auto relative = [&](uint32_t& rel) {             // exponents of f16, or false
-        const uint32_t ref = lane < 16 ? ek : ev;
-        const uint32_t w = some ? (w4 & used_bytes) | (ref & ~used_bytes) : ref;
-        const uint32_t de = (w & 0x00FF00FFu) + 0x000F000Fu - (ref & 0x00FF00FFu);
-        const uint32_t dq = ((w >> 8) & 0x00FF00FFu) + 0x000F000Fu - ((ref >> 8) & 0x00FF00FFu);
-        constexpr uint32_t C = 0x8000u - 1u - HI;      // a half that is 0 or above HI sets a top bit
-        constexpr uint32_t CC = C | (C << 16);
-        const uint32_t bad = (de | dq | (de + CC) | (dq + CC) | (de - 0x00010001u) | (dq - 0x00010001u)) & 0x80008000u;
-        rel = (de & 0x00FF00FFu) | ((dq & 0x00FF00FFu) << 8);
-        return bad == 0u && ref != 0u;
-      };
-      uint32_t rel = 0;
-      bool tame = __all_sync(0xFFFFFFFFu, relative(rel));
-      if (!tame) {
-        // new references: the slice's largest key byte; of each block of values the largest so far, which O changes to
-        const uint32_t mk = tq_max4(lane < 16 && some ? w4 & used_bytes : 0u), mv = tq_max4(lane >= 16 && some ? w4 & used_bytes : 0u);
-        const uint32_t m1 = max(max(mk & 0xFFu, (mk >> 8) & 0xFFu), max((mk >> 16) & 0xFFu, mk >> 24));
-        ek = max(m1, 1u) * 0x01010101u;
-        uint32_t to = 0;
+      uint32_t kr[2], vr[4];                           // 1..HI: code times power is exact in f16
+      auto relative = [&]() {
+        uint32_t most = 0;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint32_t x = (mv >> (8 * b)) & 0xFFu, y = (ev >> (8 * b)) & 0xFFu;
-          to |= (y == 0u || x > y + HI - 15u ? max(x, 1u) : y) << (8 * b);
+        for (int x = 0; x < 2; ++x) {
+          kr[x] = kb[x] + 15u - ek;
+          if (gone) kr[x] = (gone >> x) & 1u ? 15u : kr[x];
+          most = max(most, kr[x] - 1u);
         }
-        if (to != ev) {
-          const int sh = 8 * (DP == 128 ? g >> 1 : g >> 2);
-          const int down = int((ev >> sh) & 0xFFu) - int((to >> sh) & 0xFFu);        // 2^down, in two steps where it is small
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          vr[x] = vb[x] + 15u - ev;
+          if (gone) vr[x] = (gone >> (2 + x)) & 1u ? 15u : vr[x];
+          most = max(most, vr[x] - 1u);
+        }
+        return most < HI;
+      };
+      bool tame = __all_sync(0xFFFFFFFFu, relative() && near);
+      if (!tame) {
+        // New references: the slice's largest key byte; of each block of values (a thread's) the largest so far, which O changes to.
+        uint32_t mk = 0, mv = 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          kb[x] = (gone >> x) & 1u ? 1u : q8_byte(kb[x]);
+          mk = max(mk, kb[x]);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          vb[x] = (gone >> (2 + x)) & 1u ? 1u : q8_byte(vb[x]);
+          mv = max(mv, vb[x]);
+        }
+        ek = __reduce_max_sync(0xFFFFFFFFu, mk);
+#pragma unroll
+        for (int x = 1; x < (DP == 128 ? 8 : 16); x <<= 1) mv = max(mv, __shfl_xor_sync(0xFFFFFFFFu, mv, x));   // the lanes of a block: all four t4, two or four g
+        if (ev == 0u || mv > ev + HI - 15u) {
+          const int down = int(ev) - int(mv);          // 2^down, in two steps where it is small
           const float f = __uint_as_float(uint32_t(max(down, -126) + 127) << 23), f2 = __uint_as_float(uint32_t(max(down + 126, -126) + 127) << 23);
 #pragma unroll
           for (int nq = 0; nq < NQ; ++nq)
@@ -399,18 +485,12 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
             for (int j = 0; j < STEPS; ++j)
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[nq][j][e] = down < -126 ? o[nq][j][e] * f * f2 : o[nq][j][e] * f;
-          ev = to;
+          ev = mv;
         }
-        tame = __all_sync(0xFFFFFFFFu, relative(rel));
+        // references at which no byte in reach of one is read as another
+        near = ek >= 16u && ek <= 230u && ((narrow && g * (DP / 8) >= D) || (ev >= 16u && ev <= 230u));
+        tame = __all_sync(0xFFFFFFFFu, relative());    // with the bytes cut to their range
       }
-      ws[lane] = tame ? rel : some ? w4 : 0x01010101u;
-      __syncwarp();
-      const uint8_t *ks = reinterpret_cast<const uint8_t*>(ws), *vs = ks + 64;
-      uint32_t kb[2], vb[4];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) kb[x] = ks[(8 * x + g) * 4 + (DP == 128 ? t4 : t4 >> 1)];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) vb[x] = vs[(2 * t4 + (x & 1) + 8 * (x >> 1)) * 4 + (DP == 128 ? g >> 1 : g >> 2)];
       auto slice = [&](auto far) {
         constexpr bool FAR = decltype(far)::value;
         float sco[NQ][4] = {};
@@ -430,7 +510,7 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
               w[x][0] = y.x; w[x][1] = y.y; w[x][2] = y.z; w[x][3] = y.w;
             }
           }
-          const TqFactor f[2] = {tq_factor<E4M3>(kb[0], kb[0]), tq_factor<E4M3>(kb[1], kb[1])};
+          const TqFactor f[2] = {tq_factor<E4M3>(kr[0], kr[0]), tq_factor<E4M3>(kr[1], kr[1])};
 #pragma unroll
           for (int st = 0; st < STEPS; ++st) {
             uint32_t k4[4];
@@ -441,7 +521,7 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
             }
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq) {
-              uint2 q = qf[(nq * STEPS + st) * 32];
+              uint2 q = L::QREG ? qreg[L::QREG ? st : 0] : qf[(nq * STEPS + st) * 32];
               if (FAR) {                               // the queries themselves
                 const int d = t4 * (DP / 4) + 4 * st;
                 q = make_uint2(0u, 0u);
@@ -453,8 +533,7 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
           }
         }
         // ---- scores (keys g, g + 8; rows 2 t4, 2 t4 + 1) in units of log2; what a row does not see becomes -inf ----
-        const bool masked = nd + TQ_KEYS > 0;
-        const float kfac = FAR ? 1.0f : __uint_as_float((ek & 0xFFu) << 23);
+        const float kfac = FAR ? 1.0f : __uint_as_float(ek << 23);
         bool up = false;
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
@@ -474,7 +553,7 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int i = min(m0 + 8 * nq + 2 * t4 + e, a.rows - 1) / a.G;
-              const uint32_t bits = ta_mask32(a, p.r, i, n, nd) >> g;
+              const uint32_t bits = ta_mask32(a, p.r, i, n, int64_t(t) * TQ_KEYS - ctx) >> g;
               if (!(bits & 1u)) sco[nq][e] = -INFINITY;
               if (!(bits & 0x100u)) sco[nq][2 + e] = -INFINITY;
             }
@@ -530,8 +609,8 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
 #pragma unroll
             for (int c = 0; c < VW; ++c) w[x][c] &= ~((((w[x][c] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7);
         }
-        const TqFactor f0 = tq_factor<E4M3>(vb[0], vb[1]), f1 = tq_factor<E4M3>(vb[2], vb[3]);
-        const int e0 = int((ev >> (8 * (DP == 128 ? g >> 1 : g >> 2))) & 0xFFu);
+        const TqFactor f0 = tq_factor<E4M3>(vr[0], vr[1]), f1 = tq_factor<E4M3>(vr[2], vr[3]);
+        const int e0 = int(ev);
 #pragma unroll
         for (int j = 0; j < STEPS; ++j) {              // columns 2 j, 2 j + 1 of the thread's
           // two keys' codes of both columns, in the order that makes a pair of the keys' codes of one column
@@ -557,8 +636,9 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
     }
     // ---- the piece's result: rows 2 t4, 2 t4 + 1 of each tile, columns DP / 8 g ..; weights at most 1 from here on ----
     const int rows = min(a.rpg, a.rows - m0), d0 = g * (DP / 8);
-    const float unit = __uint_as_float(max(ev >> (8 * (DP == 128 ? g >> 1 : g >> 2)) & 0xFFu, 1u) << 23) * exp2f(-TQ_TOP);
-    const bool whole = p.whole(), head = p.t1 == p.nt;
+    const float unit = __uint_as_float(max(ev, 1u) << 23) * exp2f(-TQ_TOP);
+    const bool alone = p.t0 == p.a0 && p.t1 == p.a1, whole = alone && p.all(), head = p.t1 == p.a1;   // no other warp of the block; no other block
+    const int64_t slot = p.slot();
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
@@ -585,9 +665,15 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
           }
           if (g == 0 && a.lse) a.lse[row * a.Hq + h] = any ? (mref[nq][e] + log2f(sum)) * TA_LN2 : -INFINITY;
         } else {
-          if (g == 0) s_ml[head ? 0 : 1][warp][lr] = any ? make_float2(mref[nq][e] + TQ_TOP, sum * exp2f(-TQ_TOP)) : make_float2(-INFINITY, 0.0f);
-          // a head goes to the workspace, the tail into the ring, which is done with
-          float* to = head ? a.warp_o + (int64_t(blockIdx.x * WARPS + warp) * a.rs + lr) * D + d0 : reinterpret_cast<float*>(ring) + lr * DP + d0;
+          const float2 ml = any ? make_float2(mref[nq][e] + TQ_TOP, sum * exp2f(-TQ_TOP)) : make_float2(-INFINITY, 0.0f);
+          if (g == 0) {
+            if (alone) a.part_ml[slot * a.rs + lr] = make_float4(ml.x, ml.y, ml.y, 0.0f);
+            else s_ml[head ? 0 : 1][warp][lr] = ml;
+          }
+          // the block's part to its slot, a head to the workspace, the tail into the ring, which is done with
+          float* to = alone ? a.part_o + (slot * a.rs + lr) * D + d0
+                    : head  ? a.warp_o + (int64_t(blockIdx.x * WARPS + warp) * a.rs + lr) * D + d0
+                            : reinterpret_cast<float*>(ring) + lr * DP + d0;
           if (d0 < D) {
 #pragma unroll
             for (int j = 0; j < STEPS; j += 2)
@@ -597,7 +683,7 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
       }
     __syncwarp();
     if (lane == 0) {
-      if (!whole) {
+      if (!alone) {
         TqPart& part = head ? s_head[warp] : s_tail[warp];
         part.p = p;
         part.valid = 1;
@@ -605,64 +691,62 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
       more(kp + 2);                                    // the piece after the next, in place of the one before
     }
     __syncwarp();
-    if (np == 0) nt = piece[(kp + 1) % 3].t0;
-    np = max(np - 1, 0);
+    --np;                                              // (valid: the slice to copy next is of the piece that follows)
   }
   // copies in flight land before the block leaves its shared memory to another
   for (; used != issued; ++used) (void)ds_mbar_wait(&s_full[warp][used % NS], (used / NS) & 1u, DS_WAIT_LIMIT);
   __syncthreads();
   if (aborted()) return;
-  // ---- items that several warps of this block share: tails of warps [w0, w1), then the head of warp wh (-1: it goes on behind the block) ----
-  auto join = [&](int w0, int w1, int wh, const TaPiece& p, bool began) {
-    const int32_t n = s_len.n[p.r];
-    const int m0 = p.g * a.rpg, rows = min(a.rpg, a.rows - m0);
-    const bool whole = began && wh >= 0;
-    const int64_t slot = 2 * int64_t(blockIdx.x) + (began ? 1 : 0);
-    for (int u = tid; u < rows * (D / 4); u += L::THREADS) {
-      const int lr = u / (D / 4), d = (u - lr * (D / 4)) * 4, m = m0 + lr;
-      float M = -INFINITY, sum = 0.0f;
-      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int k = w0; k < w1; ++k)
-        if (s_tail[k].valid) M = fmaxf(M, s_ml[1][k][lr].x);
-      if (wh >= 0) M = fmaxf(M, s_ml[0][wh][lr].x);
-      auto add = [&](const float2& ml, const float4& z) {
-        const float f = ml.y == 0.0f ? 0.0f : ta_ex2(ml.x - M);
-        sum = __fmaf_rn(f, ml.y, sum);
-        if (ml.y == 0.0f) return;
-        y.x = __fmaf_rn(f, z.x, y.x);
-        y.y = __fmaf_rn(f, z.y, y.y);
-        y.z = __fmaf_rn(f, z.z, y.z);
-        y.w = __fmaf_rn(f, z.w, y.w);
-      };
-      for (int k = w0; k < w1; ++k)
-        if (s_tail[k].valid) add(s_ml[1][k][lr], *reinterpret_cast<const float4*>(smem + k * L::RING + (lr * DP + d) * 4));
-      if (wh >= 0) add(s_ml[0][wh][lr], __ldcg(reinterpret_cast<const float4*>(a.warp_o + (int64_t(blockIdx.x * WARPS + wh) * a.rs + lr) * D + d)));
-      const int i = m / a.G, h = p.hk * a.G + m - i * a.G;
-      const int64_t row = int64_t(p.r) * a.T + i;
-      const bool any = i < n && sum != 0.0f;
-      if (whole) {
-        const float inv = any ? 1.0f / sum : 0.0f;
-        uint2 z;
-        z.x = any ? tq_pack<true>(y.x * inv, y.y * inv) : 0u;
-        z.y = any ? tq_pack<true>(y.z * inv, y.w * inv) : 0u;
-        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + row * a.ldo + int64_t(h) * D + d) = z;
-        if (d == 0 && a.lse) a.lse[row * a.Hq + h] = any ? (M + log2f(sum)) * TA_LN2 : -INFINITY;
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + (slot * a.rs + lr) * D + d) = y;
-        if (d == 0) a.part_ml[slot * a.rs + lr] = any ? make_float4(M, sum, sum, 0.0f) : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-      }
+  // ---- items that several warps of this block share: the end (head) that warp w1 holds and the parts before it (tails of warps from w0 on) ----
+  int heads = 0;
+  for (int w = 0; w < WARPS; ++w) heads += s_head[w].valid;
+  const int per = min(a.rpg, a.rows) * (DP / 4);
+#pragma unroll 1
+  for (int u = tid; u < heads * per; u += L::THREADS) {
+    int q = u / per, w1 = 0;
+    const int lr = (u - q * per) / (DP / 4), d = (u % (DP / 4)) * 4;
+    for (;; ++w1)
+      if (s_head[w1].valid && q-- == 0) break;
+    const TqPiece& p = s_head[w1].p;
+    const int m = p.g * a.rpg + lr;
+    if (m >= a.rows || d >= D) continue;
+    const float4 own = __ldcg(reinterpret_cast<const float4*>(a.warp_o + (int64_t(blockIdx.x * WARPS + w1) * a.rs + lr) * D + d));
+    int w0 = w1;
+    float M = s_ml[0][w1][lr].x, sum = 0.0f;
+    while (w0 > 0) {
+      --w0;
+      if (!s_tail[w0].valid) continue;
+      M = fmaxf(M, s_ml[1][w0][lr].x);
+      if (s_tail[w0].p.t0 == s_tail[w0].p.a0) break;
     }
-  };
-  int open = -1;                                       // first warp of an item that has not ended yet
-  for (int w = 0; w < WARPS; ++w) {
-    if (s_head[w].valid) {
-      if (open < 0) join(w, w, w, s_head[w].p, false);
-      else join(open, w, w, s_tail[open].p, s_tail[open].p.t0 == 0);
-      open = -1;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](const float2& ml, const float4& z) {
+      if (ml.y == 0.0f) return;
+      const float f = ta_ex2(ml.x - M);
+      sum = __fmaf_rn(f, ml.y, sum);
+      y.x = __fmaf_rn(f, z.x, y.x);
+      y.y = __fmaf_rn(f, z.y, y.y);
+      y.z = __fmaf_rn(f, z.z, y.z);
+      y.w = __fmaf_rn(f, z.w, y.w);
+    };
+    for (int k = w0; k < w1; ++k)
+      if (s_tail[k].valid) add(s_ml[1][k][lr], *reinterpret_cast<const float4*>(smem + k * L::RING + (lr * DP + d) * 4));
+    add(s_ml[0][w1][lr], own);
+    const int i = m / a.G, h = p.hk * a.G + m - i * a.G;
+    const int64_t row = int64_t(p.r) * a.T + i, slot = p.slot();
+    const bool any = i < s_len.n[p.r] && sum != 0.0f;
+    if (p.all()) {
+      const float inv = any ? 1.0f / sum : 0.0f;
+      uint2 z;
+      z.x = any ? tq_pack<true>(y.x * inv, y.y * inv) : 0u;
+      z.y = any ? tq_pack<true>(y.z * inv, y.w * inv) : 0u;
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + row * a.ldo + int64_t(h) * D + d) = z;
+      if (d == 0 && a.lse) a.lse[row * a.Hq + h] = any ? (M + log2f(sum)) * TA_LN2 : -INFINITY;
+    } else {
+      *reinterpret_cast<float4*>(a.part_o + (slot * a.rs + lr) * D + d) = y;
+      if (d == 0) a.part_ml[slot * a.rs + lr] = any ? make_float4(M, sum, sum, 0.0f) : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
     }
-    if (s_tail[w].valid && open < 0) open = w;
   }
-  if (open >= 0) join(open, WARPS, -1, s_tail[open].p, s_tail[open].p.t0 == 0);
 }
 
 template <int DP, int NQ, bool CAP, bool E4M3>
