@@ -15,6 +15,7 @@ constexpr int QC_THREADS = 128;
 constexpr int QC_MAXT = 512;
 constexpr int QC_BATCH = 8;
 constexpr int QR_THREADS = 256;
+constexpr int QR_ROWS = 16;
 
 struct QaArgs {
   const void *q, *k, *v;
@@ -26,6 +27,25 @@ struct QaArgs {
   int64_t P;
   dspark_qcache c;
   int32_t* status;
+};
+
+// Walks items (head, x) of `per` a head, `step` apart, without a division each.
+struct QaItem {
+  int hd, x, per, shd, sx;
+  DS_DEV QaItem(int at, int per_, int step) : per(per_) {
+    hd = at / per;
+    x = at - hd * per;
+    shd = step / per;
+    sx = step - shd * per;
+  }
+  DS_DEV void next() {
+    hd += shd;
+    x += sx;
+    if (x >= per) {
+      x -= per;
+      ++hd;
+    }
+  }
 };
 
 // VEC consecutive columns as float32.
@@ -152,11 +172,12 @@ __global__ void __launch_bounds__(QA_THREADS) rope_append_q8_kernel(const QaArgs
   T* qo = reinterpret_cast<T*>(a.q_out);
   // queries. In place: a pair's two columns are written by the thread that read both.
   if (VEC > 1 || a.interleaved) {
-    const int qper = D / VEC, hq = h / VEC;            // halves: item x < hq also does the item h / VEC after it
-    for (int u = first; u < rows * a.Hq * qper; u += step) {
-      const int hv = u / qper, x = u - hv * qper, m = NR > 1 && hv >= a.Hq ? 1 : 0;
-      const int d = x * VEC;
-      if (VEC > 1 ? (!a.interleaved && d >= h && d < a.rot) : (d < a.rot && (d & 1))) continue;   // the pair's other thread does it
+    // halves: an item is VEC columns of both, or VEC columns past them; adjacent pairs: VEC columns, or (one at a time) a pair
+    const int turned = a.interleaved ? (VEC > 1 ? a.rot / VEC : a.rot / 2) : h / VEC, qper = turned + (D - a.rot) / VEC;
+    QaItem it(first, qper, step);
+    for (; it.hd < rows * a.Hq; it.next()) {
+      const int hv = it.hd, m = NR > 1 && hv >= a.Hq ? 1 : 0;
+      const int d = it.x < turned ? it.x * (a.interleaved && VEC == 1 ? 2 : VEC) : a.rot + (it.x - turned) * VEC;
       const int64_t row = row0 + m;
       const T* src = q + row * a.ldq + int64_t(hv - m * a.Hq) * D;
       T* dst = qo + row * a.ldo + int64_t(hv - m * a.Hq) * D;
@@ -182,11 +203,10 @@ __global__ void __launch_bounds__(QA_THREADS) rope_append_q8_kernel(const QaArgs
       }
       qa_store<T, VEC>(dst + d, y);
     }
-    (void)hq;
   } else {                                             // single columns, halves: one thread a pair, one a column past them
-    const int qper = h + (D - a.rot);
-    for (int u = first; u < rows * a.Hq * qper; u += step) {
-      const int hv = u / qper, x = u - hv * qper, m = NR > 1 && hv >= a.Hq ? 1 : 0;
+    QaItem it(first, h + (D - a.rot), step);
+    for (; it.hd < rows * a.Hq; it.next()) {
+      const int hv = it.hd, x = it.x, m = NR > 1 && hv >= a.Hq ? 1 : 0;
       const int64_t row = row0 + m;
       const T* src = q + row * a.ldq + int64_t(hv - m * a.Hq) * D;
       T* dst = qo + row * a.ldo + int64_t(hv - m * a.Hq) * D;
@@ -207,14 +227,14 @@ __global__ void __launch_bounds__(QA_THREADS) rope_append_q8_kernel(const QaArgs
   }
   // keys, then values: the block's threads stay together for the shuffles
   bool odd = false;                                    // a number that is not finite was among them
-  const int total = rows * 2 * Hk * per;               // per row: keys' heads, values' heads
-  for (int u0 = first - tid; u0 < total; u0 += step) {
-    const int u = u0 + tid;
-    const int hv = u / per, x = u - hv * per, m = NR > 1 && hv >= 2 * Hk ? 1 : 0, kv = hv - m * 2 * Hk;
+  const int heads = rows * 2 * Hk;                     // per row: keys' heads, values' heads
+  QaItem it(first, per, step);
+  for (int u0 = first - tid; u0 < heads * per; u0 += step, it.next()) {
+    const int hv = it.hd, x = it.x, m = NR > 1 && hv >= 2 * Hk ? 1 : 0, kv = hv - m * 2 * Hk;
     const bool value = kv >= Hk;
     const int hd = value ? kv - Hk : kv, d = x * VEC;
-    const bool there = u < total && d < D;
-    const Q8Slot at = s_slot[m];
+    const bool there = hv < heads && d < D;
+    const Q8Slot at = s_slot[min(m, NR - 1)];
     float y[VEC] = {};
     if (there && at.at >= 0) {
       const T* src = value ? reinterpret_cast<const T*>(a.v) + (row0 + m) * a.ldv + int64_t(hd) * D
@@ -227,7 +247,6 @@ __global__ void __launch_bounds__(QA_THREADS) rope_append_q8_kernel(const QaArgs
     for (int e = 0; e < VEC; ++e) {
       const bool finite = fabsf(y[e]) < INFINITY;
       odd = odd || !finite;
-      if (y[e] != y[e]) y[e] = 0.0f;
       most = fmaxf(most, finite ? fabsf(y[e]) : 0.0f);
     }
 #pragma unroll
@@ -237,12 +256,9 @@ __global__ void __launch_bounds__(QA_THREADS) rope_append_q8_kernel(const QaArgs
     const float inv = __uint_as_float((254u - byte) << 23);
     uint8_t* dst = reinterpret_cast<uint8_t*>(value ? a.c.v : a.c.k) + at.at + int64_t(hd) * a.c.head_stride + d;
     if constexpr (VEC == 8) {
-      uint32_t w[2] = {0u, 0u};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e >> 2] |= q8_code(y[e], inv, e4m3) << (8 * (e & 3));
-      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(dst) = make_uint2(q8_codes(y[0], y[1], y[2], y[3], inv, e4m3), q8_codes(y[4], y[5], y[6], y[7], inv, e4m3));
     } else {
-      *dst = uint8_t(q8_code(y[0], inv, e4m3));
+      *dst = uint8_t(q8_codes(y[0], 0.0f, 0.0f, 0.0f, inv, e4m3));
     }
     if (x % GROUP == 0) (value ? a.c.v_scale : a.c.k_scale)[at.scale + int64_t(hd) * a.c.scale_head_stride + x / GROUP] = uint8_t(byte);
   }
@@ -359,44 +375,84 @@ struct QrArgs {
   int32_t* status;
 };
 
-// VEC codes a thread, the items of a slot's heads (keys, then values) going over the threads side by side. Bound by HBM: 1 + 1/32
-// bytes read and 2 or 4 written a column.
+// A block reads QR_ROWS slots: their places are looked up once, then the threads go over the slots' heads (keys, then values) VEC codes at a
+// time, side by side. Bound by HBM: 1 + 1/32 bytes read and 2 or 4 written a column.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(QR_THREADS) cache_read_q8_kernel(const QrArgs a) {
+  __shared__ Q8Slot s_slot[QR_ROWS];                   // at -1: a slot without a place; -2: a row that is left as it is
+  const int tid = threadIdx.x;
+  const int64_t row0 = int64_t(blockIdx.x) * QR_ROWS;
   ds_pdl_trigger();
   ds_pdl_wait();
-  const int D = a.c.head_dim, per = D / VEC, items = 2 * a.c.heads * per;
-  const bool e4m3 = a.c.code == DSPARK_E4M3;
-  const int64_t all = a.rows * items, step = int64_t(gridDim.x) * QR_THREADS;
-  for (int64_t u = int64_t(blockIdx.x) * QR_THREADS + threadIdx.x; u < all; u += step) {
-    const int64_t row = u / items;
-    const int x = int(u - row * items), hv = x / per, d = (x - hv * per) * VEC;
-    const int64_t r = row / a.S, i = row - r * a.S;
-    int32_t n = a.n[r];
-    const int32_t s0 = a.start ? a.start[r] : 0;
-    if (n < 0 || n > a.S || s0 < 0) {
-      ds_set_error(a.status, DSPARK_EINVAL);
-      n = 0;
-    }
-    if (i >= n) continue;
-    const Q8Slot at = q8_slot(a.c, r, int64_t(s0) + i);
-    if (at.at < 0) ds_set_error(a.status, DSPARK_ERANGE);
-    const bool value = hv >= a.c.heads;
-    const int hd = value ? hv - a.c.heads : hv;
-    float y[VEC] = {};
-    if (at.at >= 0) {
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(value ? a.c.v : a.c.k) + at.at + int64_t(hd) * a.c.head_stride + d;
-      const uint8_t* ss = (value ? a.c.v_scale : a.c.k_scale) + at.scale + int64_t(hd) * a.c.scale_head_stride;
-      const float f = q8_power(ss[d / Q8_BLOCK]);
-      if constexpr (VEC == 8) {
-        const uint2 w = *reinterpret_cast<const uint2*>(src);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = q8_number((e < 4 ? w.x : w.y) >> (8 * (e & 3)), e4m3) * f;
-      } else {
-        y[0] = q8_number(*src, e4m3) * f;
+  if (tid < QR_ROWS) {
+    Q8Slot at{-2, -2};
+    if (row0 + tid < a.rows) {
+      const int64_t r = (row0 + tid) / a.S, i = row0 + tid - r * a.S;
+      int32_t n = a.n[r];
+      const int32_t s0 = a.start ? a.start[r] : 0;
+      if (n < 0 || n > a.S || s0 < 0) {
+        ds_set_error(a.status, DSPARK_EINVAL);
+        n = 0;
+      }
+      if (i < n) {
+        at = q8_slot(a.c, r, int64_t(s0) + i);
+        if (at.at < 0) ds_set_error(a.status, DSPARK_ERANGE);
       }
     }
-    qa_store<T, VEC>(reinterpret_cast<T*>(value ? a.v : a.k) + row * a.ld + int64_t(hd) * D + d, y);
+    s_slot[tid] = at;
+  }
+  __syncthreads();
+  const int D = a.c.head_dim, per = D / VEC, items = 2 * a.c.heads * per;
+  const bool e4m3 = a.c.code == DSPARK_E4M3;
+  int m = tid / items, x = tid - m * items;            // slot of the block, item of the slot
+  while (m < QR_ROWS) {
+    // four items' codes on their way together
+    constexpr int AT = 4;
+    uint4 w[AT];
+    float f[AT];
+    T* to[AT];
+#pragma unroll
+    for (int c = 0; c < AT; ++c) {
+      to[c] = nullptr;
+      w[c] = make_uint4(0u, 0u, 0u, 0u);
+      f[c] = 0.0f;
+      if (m >= QR_ROWS) continue;
+      const Q8Slot at = s_slot[m];
+      const int hv = x / per, d = (x - hv * per) * VEC;
+      const bool value = hv >= a.c.heads;
+      const int hd = value ? hv - a.c.heads : hv;
+      if (at.at != -2) to[c] = reinterpret_cast<T*>(value ? a.v : a.k) + (row0 + m) * a.ld + int64_t(hd) * D + d;
+      if (at.at >= 0) {
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(value ? a.c.v : a.c.k) + at.at + int64_t(hd) * a.c.head_stride + d;
+        f[c] = q8_power((value ? a.c.v_scale : a.c.k_scale)[at.scale + int64_t(hd) * a.c.scale_head_stride + d / Q8_BLOCK]);
+        if constexpr (VEC == 16) {
+          w[c] = __ldcs(reinterpret_cast<const uint4*>(src));
+        } else if constexpr (VEC == 8) {
+          const uint2 y = __ldcs(reinterpret_cast<const uint2*>(src));
+          w[c].x = y.x;
+          w[c].y = y.y;
+        } else {
+          w[c].x = *src;
+        }
+      }
+      for (x += QR_THREADS; x >= items && m < QR_ROWS; x -= items) ++m;
+    }
+#pragma unroll
+    for (int c = 0; c < AT; ++c) {
+      if (to[c] == nullptr) continue;
+      if constexpr (VEC == 1) {
+        const float y[1] = {q8_number(w[c].x, e4m3) * f[c]};
+        qa_store<T, 1>(to[c], y);
+      } else {
+#pragma unroll
+        for (int u = 0; u < VEC / 8; ++u) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = q8_number((u ? (e < 4 ? w[c].z : w[c].w) : (e < 4 ? w[c].x : w[c].y)) >> (8 * (e & 3)), e4m3) * f[c];
+          qa_store<T, 8>(to[c] + 8 * u, y);
+        }
+      }
+    }
   }
 }
 
@@ -449,10 +505,13 @@ extern "C" dspark_status dspark_cache_read_q8(const dspark_qcache* cache, const 
   QrArgs a{*cache, start, n, R * S, ld, S, k_out, v_out, dev_status};
   a.c.layer_stride = a.c.scale_layer_stride = 0;
   const bool vec = q8_codes_aligned(&a.c, 8) && ds_aligned(k_out, 16) && ds_aligned(v_out, 16) && (ld * int64_t(e)) % 16 == 0;
-  const int64_t all = a.rows * 2 * cache->heads * (cache->head_dim / (vec ? 8 : 1));
-  const dim3 grid(unsigned(std::min<int64_t>(ds_ceil_div(all, QR_THREADS), int64_t(ds_num_sms()) * 64)));
+  const dim3 grid(unsigned(ds_ceil_div(a.rows, QR_ROWS)));
+  const bool v16 = vec && cache->head_dim % 16 == 0 && q8_codes_aligned(&a.c, 16);
   auto go = [&](auto kern) { return ds_launch(kern, grid, dim3(QR_THREADS), 0, stream, a); };
-  if (dtype == DSPARK_BF16) DS_CUDA_TRY(vec ? go(cache_read_q8_kernel<__nv_bfloat16, 8>) : go(cache_read_q8_kernel<__nv_bfloat16, 1>));
-  else DS_CUDA_TRY(vec ? go(cache_read_q8_kernel<float, 8>) : go(cache_read_q8_kernel<float, 1>));
+  if (dtype == DSPARK_BF16) {
+    DS_CUDA_TRY((v16 ? go(cache_read_q8_kernel<__nv_bfloat16, 16>) : vec ? go(cache_read_q8_kernel<__nv_bfloat16, 8>) : go(cache_read_q8_kernel<__nv_bfloat16, 1>)));
+  } else {
+    DS_CUDA_TRY((v16 ? go(cache_read_q8_kernel<float, 16>) : vec ? go(cache_read_q8_kernel<float, 8>) : go(cache_read_q8_kernel<float, 1>)));
+  }
   return DSPARK_OK;
 }

@@ -2,8 +2,6 @@
 // checks that every entry point makes of a dspark_qcache.
 #pragma once
 
-#include <cuda_fp8.h>
-
 #include "dspark_common.cuh"
 #include "host_common.h"
 
@@ -33,12 +31,22 @@ DS_DEV uint32_t q8_choose(float m, bool e4m3) {
   return uint32_t(min(max(e, -126), 118) + 127);
 }
 
-// Code of y under 2^-e (`inv`).
-DS_DEV uint32_t q8_code(float y, float inv, bool e4m3) {
-  const float lim = e4m3 ? 448.0f : 127.0f;
-  const float z = fminf(fmaxf(y * inv, -lim), lim);     // infinities end here; what is not a number was replaced
-  if (e4m3) return uint32_t(__nv_cvt_float_to_fp8(z, __NV_SATFINITE, __NV_E4M3));
-  return uint32_t(__float2int_rn(z)) & 0xFFu;
+// Codes of four numbers under 2^-e (`inv`), the first in the low byte. Infinities become the largest code, what is not a number 0. E4M3: the
+// conversion rounds to nearest, ties to even, and saturates. INT8: adding 1.5 * 2^23 leaves the rounded number in the low bits.
+DS_DEV uint32_t q8_codes(float y0, float y1, float y2, float y3, float inv, bool e4m3) {
+  float z[4] = {y0 * inv, y1 * inv, y2 * inv, y3 * inv};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) z[e] = z[e] == z[e] ? z[e] : 0.0f;
+  if (e4m3) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(z[1]), "f"(z[0]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(z[3]), "f"(z[2]));
+    return uint32_t(lo) | (uint32_t(hi) << 16);
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(fminf(fmaxf(z[e], -127.0f), 127.0f) + 12582912.0f);
+  return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
 }
 
 // Where slot s of request r lies: offsets of its codes and of its scales (head 0, column 0, layer 0); at < 0: it has no place.
@@ -74,4 +82,8 @@ static inline bool q8_codes_aligned(const dspark_qcache* c, int64_t a) {
 static inline bool q8_scales_aligned(const dspark_qcache* c, int64_t a) {
   return ds_aligned(c->k_scale, size_t(a)) && ds_aligned(c->v_scale, size_t(a)) && c->scale_page_stride % a == 0 &&
          c->scale_token_stride % a == 0 && c->scale_head_stride % a == 0 && c->scale_layer_stride % a == 0;
+}
+// The scale bytes of a box of slots (`bytes` of them, a multiple of 16, slots side by side) start on 16-byte boundaries.
+static inline bool q8_scales_box(const dspark_qcache* c, int64_t bytes) {
+  return bytes % 16 == 0 && ds_aligned(c->k_scale, 16) && ds_aligned(c->v_scale, 16) && c->scale_page_stride % 16 == 0 && c->scale_head_stride % 16 == 0;
 }

@@ -13,6 +13,7 @@ struct TaQ8 {
   const uint8_t *k_scale, *v_scale;
   int64_t page_stride, token_stride, head_stride;   // of the scales
   int32_t e4m3, vec8, vec4;    // rows of codes start on 8-byte boundaries, of scales on 4-byte ones
+  int32_t bulk;                // the scale bytes of a box of slots are one run that a bulk copy takes
 };
 
 struct TaArgs {

@@ -76,6 +76,8 @@ extern "C" dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, ds
   const int cols = D <= 64 ? 64 : 128;
   const bool maps = tc && tq_tensor_map(&mk, cache->k, *cache, cols, box) && tq_tensor_map(&mv, cache->v, *cache, cols, box);
   a.box = box;
+  const int nb = q8_blocks(int(D));
+  a.q8.bulk = cache->scale_token_stride == nb && (box * nb) % 16 == 0 && q8_scales_box(&one, box * nb);
   if (maps && few) {
     a.kt = 16;
     a.rpg = a.rows <= 8 ? 8 : a.rows <= 16 ? 16 : 32;

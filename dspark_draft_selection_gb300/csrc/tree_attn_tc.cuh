@@ -43,14 +43,15 @@ template <int DP, bool TWO, bool Q8>
 __host__ __device__ constexpr int ta_stages() {
   return Q8 ? (DP == 128 ? 3 : 6) : DP == 128 ? (TWO ? 4 : 5) : 8;
 }
-// Codes: threads with the four warps that widen them, the ring that TMA fills, and registers of a thread of the first four warps, the softmax
-// groups and the widening warps (of 128 at launch: 80 + 2 x 168 + 96 = 4 x 128).
-// Three stages are the fewest of either ring: a copying warp goes past up to two tiles of the other's, and a phase later than the next would
-// look to it like the one before.
-constexpr int TA_THREADS_Q8 = 512, TA_NRAW = 3;
+// Codes: threads with the four warps that widen them, the ring that TMA fills.
+constexpr int TA_THREADS_Q8 = 512;
+template <bool TWO>
+__host__ __device__ constexpr int ta_raw_stages() {      // of the ring that TMA fills with codes
+  return TWO ? 3 : 4;
+}
 template <int DP, bool TWO, bool Q8>
 __host__ __device__ constexpr size_t ta_smem() {
-  return 1024 + size_t(DP / 64) * TA_CHUNK * ((TWO ? 2 : 1) + ta_stages<DP, TWO, Q8>()) + (Q8 ? TA_NRAW * size_t(TA_KT) * DP : 0);
+  return 1024 + size_t(DP / 64) * TA_CHUNK * ((TWO ? 2 : 1) + ta_stages<DP, TWO, Q8>()) + (Q8 ? ta_raw_stages<TWO>() * size_t(TA_KT) * DP : 0);
 }
 
 // 4-D tiled TMA load (column, place in page, head, page), what lies outside the tensor reading as zero,
@@ -270,7 +271,7 @@ __device__ __noinline__ void ta_add_odd(const TaArgs& a, int r, int32_t ctx, int
   }
 }
 
-// A row of codes of one key (raw: its tile as TMA left it) as bf16 numbers into the tile that the MMAs take. A thread a key; `w4`: the scale bytes of its
+// A row of codes of one key as bf16 numbers into the tile that the MMAs take. A thread a key; `w4`: the scale bytes of its
 // blocks. Rows go to different banks within each 8 lanes on both sides. E4M3: the seven bits under the sign go to bits 10..4 of a bf16 number,
 // which is then the number times 2^-120; INT8: 128 + (low seven bits) - 128 (1 + sign).
 template <int DP, bool E4M3>
@@ -290,8 +291,8 @@ DS_DEV void ta_widen_row(const uint8_t* raw, uint8_t* tile, int row, uint32_t w4
     asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(m), "r"(c));
     return r;
   };
-#pragma unroll 2
-  for (int c = 0; c < DP / 16; ++c) {
+#pragma unroll 1
+  for (int c = 0; c < DP / 16; ++c) {                  // (a loop: unrolled, its code takes the others' place in the instruction caches)
     const uint4 x = *reinterpret_cast<const uint4*>(raw + row * DP + ((c ^ (DP == 128 ? row & 7 : (row >> 1) & 3)) << 4));
     const uint32_t b = q8_byte((w4 >> (8 * (c >> 1))) & 0xFFu);
     const uint32_t f = (E4M3 ? min(b + 120u, 254u) : b) * 0x00800080u, f2 = (127u + (b > 134u ? b - 134u : 0u)) * 0x00800080u;
@@ -315,23 +316,36 @@ DS_DEV void ta_widen_row(const uint8_t* raw, uint8_t* tile, int row, uint32_t w4
   }
 }
 
+// Tile number k of a piece of npt tiles in the ring's order: K0 V0 K1 V1 .. for two row tiles, else K0 K1 V0 K2 V1 K3 ..
+template <bool TWO>
+DS_DEV int ta_ring_tile(int k, int npt, bool& isv) {
+  if (TWO || npt == 1) {
+    isv = k & 1;
+    return k >> 1;
+  }
+  isv = k >= 2 * npt - 2 || (k > 0 && !(k & 1));
+  return k == 0 ? 0 : k == 2 * npt - 1 ? npt - 1 : isv ? k / 2 - 1 : (k + 1) / 2;
+}
+
 template <int DP, bool TWO, bool CAP, bool Q8>
 __global__ void __launch_bounds__(Q8 ? TA_THREADS_Q8 : TA_THREADS, 1) tree_attn_tc_kernel(const TaArgs a,
                                                                      const __grid_constant__ CUtensorMap tmK,
                                                                      const __grid_constant__ CUtensorMap tmV) {
   constexpr int NS = ta_stages<DP, TWO, Q8>();
+  constexpr int NRAW = ta_raw_stages<TWO>();
   constexpr uint32_t RAW = TA_KT * DP;                 // bytes of a tile of codes
   constexpr int NC = DP / 64;                          // 64-column chunks
   constexpr uint32_t STAGE = NC * TA_CHUNK;
   constexpr uint32_t TS = 0, TO = 256;                 // tensor memory: S of group g at 128 g, O at 256 + DP g
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[NS], s_empty[NS], s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_ofull, s_ofree, s_mlfull, s_drain;
-  __shared__ uint32_t s_tmem, s_seq[NS];               // s_seq: sequence number + 1 of a stage's last copy
+  __shared__ uint32_t s_tmem, s_seq[Q8 ? NRAW : NS];               // s_seq: sequence number + 1 of a stage's last copy
   __shared__ int s_abort;
   __shared__ TaLens s_len;
   __shared__ float4 s_ml[2][2][128];                   // [piece parity][group][row]
   __shared__ uint4 s_odd[3][Q8 ? 1 : TA_MAXT / 128];   // [piece modulo 3]: a bit for every node with a value that is not finite
-  __shared__ uint64_t s_rfull[TA_NRAW], s_rempty[TA_NRAW];   // the ring of codes
+  __shared__ uint64_t s_rfull[NRAW], s_rempty[NRAW];   // the ring of codes and of their scale bytes
+  __shared__ __align__(16) uint8_t s_scale[Q8 ? NRAW : 1][Q8 ? 4 * TA_KT : 16];
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -348,9 +362,10 @@ __global__ void __launch_bounds__(Q8 ? TA_THREADS_Q8 : TA_THREADS, 1) tree_attn_
     for (int s = 0; s < NS; ++s) {
       ds_mbar_init(&s_full[s], Q8 ? 4 : 1);
       ds_mbar_init(&s_empty[s], 1);
-      s_seq[s] = 0;
+      if (!Q8) s_seq[s] = 0;
     }
-    for (int s = 0; Q8 && s < TA_NRAW; ++s) {
+    for (int s = 0; Q8 && s < NRAW; ++s) {
+      s_seq[s] = 0;
       ds_mbar_init(&s_rfull[s], 1);
       ds_mbar_init(&s_rempty[s], 4);
     }
@@ -380,96 +395,68 @@ __global__ void __launch_bounds__(Q8 ? TA_THREADS_Q8 : TA_THREADS, 1) tree_attn_
     s_abort = 1;
     return false;
   };
-  if constexpr (Q8) {
-    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    else if (warp < 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-  }
   TaWalk walk;
   walk.init(s_len);
   TaPiece p;
 
   if (Q8 && warp >= 12) {
-    // ---- codes to bf16 numbers, tile after tile in the ring's order; a thread a key, whose page is asked for two tiles and whose scale bytes
-    // one tile before they are needed ----
-    const int row = tid - 384;
-    const int D = a.c.head_dim, nb = q8_blocks(D);
-    const bool words = nb == 4 && a.q8.vec4 != 0;
+    // ---- codes to bf16 numbers, tile after tile in the ring's order, a thread a key ----
+    const int row = tid - 384, nb = q8_blocks(a.c.head_dim);
     uint32_t sq = 0;
     bool ok = true;
     while (ok && walk.next(s_len, a, p)) {
-      const uint32_t len = uint32_t(s_len.ctx[p.r]) + uint32_t(s_len.n[p.r]), page = uint32_t(a.c.page_size);
-      const int32_t* table = a.c.page_table + int64_t(p.r) * a.c.ld_table;
       const int npt = p.t1 - p.t0;
-      // the piece's tile number k of the ring: (tile, whether it holds values)
-      auto which = [&](int k, bool& isv) {
-        if (TWO || npt == 1) {
-          isv = k & 1;
-          return k >> 1;
-        }
-        isv = k >= 2 * npt - 2 || (k > 0 && !(k & 1));
-        return k == 0 ? 0 : k == 2 * npt - 1 ? npt - 1 : isv ? k / 2 - 1 : (k + 1) / 2;
-      };
-      auto look_up = [&](int k, uint32_t& place) {     // page of this thread's key of tile k, or -1
-        bool isv;
-        if (k >= 2 * npt) return int32_t(-1);
-        const uint32_t key = uint32_t(p.t0 + which(k, isv)) * TA_KT + row;
-        if (key >= len) return int32_t(-1);
-        const uint32_t e = key / page;
-        place = key - e * page;
-        return table[e];
-      };
-      auto scales = [&](int k, int32_t pg, uint32_t place) {
-        bool isv;
-        if (k >= 2 * npt || uint32_t(pg) >= uint32_t(a.c.num_pages)) return 0u;      // (the copying warps report such a page)
-        which(k, isv);
-        const uint8_t* at = (isv ? a.q8.v_scale : a.q8.k_scale) + int64_t(pg) * a.q8.page_stride + int64_t(place) * a.q8.token_stride + p.hk * a.q8.head_stride;
-        if (words) return *reinterpret_cast<const uint32_t*>(at);
-        uint32_t w = 0;
-        for (int b = 0; b < nb; ++b) w |= uint32_t(at[b]) << (8 * b);
-        return w;
-      };
-      uint32_t pl1 = 0, pl2 = 0;
-      int32_t pg1 = look_up(0, pl1);
-      uint32_t w0 = scales(0, pg1, pl1);
-      pg1 = look_up(1, pl1);
       for (int k = 0; k < 2 * npt; ++k, ++sq) {
-        const int32_t pg2 = look_up(k + 2, pl2);
-        const uint32_t w1 = scales(k + 1, pg1, pl1);
-        const uint32_t rs = sq % TA_NRAW, s = sq % NS;
-        ok = wait(&s_rfull[rs], sq / TA_NRAW, DS_WAIT_LIMIT) && wait(&s_empty[s], sq / NS + 1, DS_WAIT_LIMIT);
+        const uint32_t rs = sq % NRAW, s = sq % NS;
+        uint32_t w4 = 0;
+        if (!a.q8.bulk) {                              // scale bytes that no bulk copy takes
+          bool isv;
+          const uint32_t key = uint32_t(p.t0 + ta_ring_tile<TWO>(k, npt, isv)) * TA_KT + row;
+          int64_t at = -1, sc = 0;
+          if (key < uint32_t(s_len.ctx[p.r]) + uint32_t(s_len.n[p.r])) at = ta_slot_q8(a, p.r, key, sc);
+          const uint8_t* src = (isv ? a.q8.v_scale : a.q8.k_scale) + sc + p.hk * a.q8.head_stride;
+          for (int b = 0; b < nb && at >= 0; ++b) w4 |= uint32_t(src[b]) << (8 * b);
+        }
+        ok = wait(&s_rfull[rs], sq / NRAW, DS_WAIT_LIMIT) && wait(&s_empty[s], sq / NS + 1, DS_WAIT_LIMIT);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        if (a.q8.e4m3) ta_widen_row<DP, true>(sC + rs * RAW, sR + s * STAGE, row, w0);
-        else ta_widen_row<DP, false>(sC + rs * RAW, sR + s * STAGE, row, w0);
+        const uint8_t* bytes = s_scale[rs];
+        if (a.q8.bulk) {
+          if (nb == 4) w4 = reinterpret_cast<const uint32_t*>(bytes)[row];
+          else if (nb == 2) w4 = reinterpret_cast<const uint16_t*>(bytes)[row];
+          else
+            for (int b = 0; b < nb; ++b) w4 |= uint32_t(bytes[row * nb + b]) << (8 * b);
+        }
+        if (a.q8.e4m3) ta_widen_row<DP, true>(sC + rs * RAW, sR + s * STAGE, row, w4);
+        else ta_widen_row<DP, false>(sC + rs * RAW, sR + s * STAGE, row, w4);
         ds_fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           ds_mbar_arrive(&s_rempty[rs]);
           ds_mbar_arrive(&s_full[s]);
         }
-        w0 = w1;
-        pg1 = pg2;
-        pl1 = pl2;
       }
     }
   } else if (warp == 0 || warp == 2) {
     // ---- key tiles (warp 0) and value tiles (warp 2): lane b looks up the page of box b (keys b * box ..),
     // then the boxes go out one after the other. The copy of a box past the last key, or of a page that
     // does not exist, names a page past the last and reads zeros. The tiles lie in the ring in the order in
-    // which the MMA warp takes them: K0 V0 K1 V1 .. for two row tiles, else K0 K1 V0 K2 V1 K3 .. ----
-    const bool isv = warp == 2;
+    // which the MMA warp takes them: K0 V0 K1 V1 .. for two row tiles, else K0 K1 V0 K2 V1 K3 ..
+    // (codes: warp 0 copies both, in that order). ----
+    bool isv = warp == 2;
     const CUtensorMap* tm = isv ? &tmV : &tmK;
     const int box = a.box, nbox = TA_KT / box;
     uint32_t base = 0;                                 // sequence number of the piece's first tile
     bool ok = true;
-    while (ok && walk.next(s_len, a, p)) {
+    const uint32_t sbytes = uint32_t(box * q8_blocks(a.c.head_dim));     // scale bytes of a box
+    while (ok && !(Q8 && warp == 2) && walk.next(s_len, a, p)) {
       const uint32_t len = uint32_t(s_len.ctx[p.r]) + uint32_t(s_len.n[p.r]), page = uint32_t(a.c.page_size);
       const int32_t* table = a.c.page_table + int64_t(p.r) * a.c.ld_table;
       const int npt = p.t1 - p.t0;
       int32_t place = 0, pg = 0;
       auto look_up = [&](int t) {                      // (page, place) of this lane's box of the piece's tile t
         pg = int32_t(a.c.num_pages);
+        if (Q8 && t < 2 * npt) t = ta_ring_tile<TWO>(t, npt, isv);
         const uint32_t key = uint32_t(p.t0 + t) * TA_KT + uint32_t(lane * box);
         if (lane < nbox && t < npt && key < len) {
           const uint32_t e = key / page;
@@ -482,16 +469,19 @@ __global__ void __launch_bounds__(Q8 ? TA_THREADS_Q8 : TA_THREADS, 1) tree_attn_
         }
       };
       look_up(0);
-      for (int t = 0; t < npt; ++t) {
-        const uint32_t sq = base + (TWO ? 2 * t + (isv ? 1 : 0) : isv ? min(npt, t + 2) + t : t < 2 ? t : 2 * t - 1);
-        const uint32_t s = sq % (Q8 ? TA_NRAW : NS);
+      for (int t = 0; t < (Q8 ? 2 * npt : npt); ++t) {
+        const uint32_t sq = base + (Q8 ? t : TWO ? 2 * t + (isv ? 1 : 0) : isv ? min(npt, t + 2) + t : t < 2 ? t : 2 * t - 1);
+        const uint8_t* scale = (isv ? a.q8.v_scale : a.q8.k_scale) + p.hk * a.q8.head_stride;
+        const uint32_t boxes = Q8 && a.q8.bulk ? __popc(__ballot_sync(0xFFFFFFFFu, lane < nbox && pg != int32_t(a.c.num_pages))) : 0u;
+        if (Q8) tm = isv ? &tmV : &tmK;
+        const uint32_t s = sq % (Q8 ? NRAW : NS);
         const int32_t pg_t = pg, place_t = place;
         look_up(t + 1);                                // on its way while this tile waits for its stage
-        ok = __all_sync(0xFFFFFFFFu, Q8 ? wait(&s_rempty[s], (sq / TA_NRAW + 1), DS_WAIT_LIMIT) : wait(&s_empty[s], (sq / NS + 1), DS_WAIT_LIMIT));
+        ok = __all_sync(0xFFFFFFFFu, Q8 ? wait(&s_rempty[s], (sq / NRAW + 1), DS_WAIT_LIMIT) : wait(&s_empty[s], (sq / NS + 1), DS_WAIT_LIMIT));
         if (!ok) break;
         if (lane == 0) {
           s_seq[s] = sq + 1;
-          ds_mbar_arrive_expect_tx(Q8 ? &s_rfull[s] : &s_full[s], Q8 ? RAW : STAGE);
+          ds_mbar_arrive_expect_tx(Q8 ? &s_rfull[s] : &s_full[s], Q8 ? RAW + boxes * sbytes : STAGE);
         }
         __syncwarp();
 #pragma unroll 1
@@ -499,6 +489,8 @@ __global__ void __launch_bounds__(Q8 ? TA_THREADS_Q8 : TA_THREADS, 1) tree_attn_
           const int32_t pb = __shfl_sync(0xFFFFFFFFu, pg_t, b), lb = __shfl_sync(0xFFFFFFFFu, place_t, b);
           if constexpr (Q8) {
             ta_tma_load(sC + s * RAW + b * box * DP, tm, 0, lb, p.hk, pb, &s_rfull[s]);
+            if (a.q8.bulk && pb != int32_t(a.c.num_pages) && lane == 0)      // a box's scale bytes lie side by side
+              ds_bulk_g2s(s_scale[s] + b * sbytes, scale + int64_t(pb) * a.q8.page_stride + int64_t(lb) * a.q8.token_stride, sbytes, &s_rfull[s]);
           } else {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -938,8 +930,8 @@ __global__ void __launch_bounds__(Q8 ? TA_THREADS_Q8 : TA_THREADS, 1) tree_attn_
   // issued and does every warp know of the wait.
   if (warp == 1) {
     if (aborted())
-      for (int k = 0; k < (Q8 ? TA_NRAW : NS); ++k)
-        if (s_seq[k]) (void)ds_mbar_wait(Q8 ? &s_rfull[k] : &s_full[k], ((s_seq[k] - 1) / (Q8 ? TA_NRAW : NS)) & 1u, DS_WAIT_LIMIT);
+      for (int k = 0; k < (Q8 ? NRAW : NS); ++k)
+        if (s_seq[k]) (void)ds_mbar_wait(Q8 ? &s_rfull[k] : &s_full[k], ((s_seq[k] - 1) / (Q8 ? NRAW : NS)) & 1u, DS_WAIT_LIMIT);
     __syncwarp();
     ds_tc_fence_after();
     ds_tmem_dealloc(tmem, 512);

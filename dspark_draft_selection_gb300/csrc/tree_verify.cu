@@ -13,7 +13,7 @@ namespace {
 using rs::FF;
 
 constexpr int TV_MAXT = 512;
-constexpr int TV_THREADS = 256;
+constexpr int TV_THREADS = 512;
 constexpr int TV_WARPS = TV_THREADS / 32;
 constexpr int TV_MAXC = 8;                   // blocks of a cluster
 
@@ -58,6 +58,13 @@ DS_DEV FF tv_term(float p, float q, const FF& a) {
 DS_DEV void tv_add(FF& acc, const FF& t) {
   rs::ff_add(acc, t.hi);
   acc.lo = __fadd_rn(acc.lo, t.lo);
+}
+
+// Entries i .. i + 3 of a row (VEC 4: 16-byte aligned, i a multiple of 4), 0 from `hi` on.
+template <int VEC>
+DS_DEV float4 tv_load(const float* row, int64_t i, int64_t hi) {
+  if (VEC == 4 && i + 4 <= hi) return __ldg(reinterpret_cast<const float4*>(row + i));
+  return make_float4(i < hi ? row[i] : 0.0f, i + 1 < hi ? row[i + 1] : 0.0f, i + 2 < hi ? row[i + 2] : 0.0f, i + 3 < hi ? row[i + 3] : 0.0f);
 }
 
 DS_DEV void tv_put_remote(FF* at, int rank, const FF& x) {      // the same place of another block of the cluster
@@ -194,31 +201,47 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
       const bool minus = Q && (fa.hi != 0.0f || fa.lo != 0.0f) && !plain;
       // refused children of this node, without q: their ids count as 0
       auto gone = [&](int64_t id) {
-        if (Q || plain) return false;
-        for (int k = s.refused; k < TV_MAXT; k = s.next[k])
-          if (s.tok[k] == id) return true;
+        if constexpr (!Q) {
+          for (int k = plain ? TV_MAXT : s.refused; k < TV_MAXT; k = s.next[k])
+            if (s.tok[k] == id) return true;
+        }
         return false;
       };
       auto span = [&](int64_t i0, int64_t i1) {        // whether any refused id lies there
-        if (Q || plain) return false;
-        for (int k = s.refused; k < TV_MAXT; k = s.next[k])
-          if (s.tok[k] >= i0 && s.tok[k] < i1) return true;
+        if constexpr (!Q) {
+          for (int k = plain ? TV_MAXT : s.refused; k < TV_MAXT; k = s.next[k])
+            if (s.tok[k] >= i0 && s.tok[k] < i1) return true;
+        }
         return false;
       };
       if (!known) {
         const bool some = span(lo, hi);
         FF acc[4] = {};
-        if (minus) {
-          for (int64_t i = lo + lane * VEC; i < hi; i += 32 * VEC) {
+        // four vectors of each row on their way together
+        for (int64_t i = lo + lane * 4; i < hi; i += 32 * 16) {
+          float4 x[4], y[4];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-              if (VEC == 1 || i + e < hi) tv_add(acc[e], tv_term<true>(pr[i + e], qr[i + e], fa));
+          for (int c = 0; c < 4; ++c) {
+            x[c] = tv_load<VEC>(pr, i + 128 * c, hi);
+            if (minus) y[c] = tv_load<VEC>(qr, i + 128 * c, hi);
           }
-        } else {
-          for (int64_t i = lo + lane * VEC; i < hi; i += 32 * VEC) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-              if (VEC == 1 || i + e < hi) tv_add(acc[e], tv_term<false>(some && gone(i + e) ? 0.0f : pr[i + e], 0.0f, fa));
+          for (int c = 0; c < 4; ++c) {
+            if (some) {
+              const int64_t id = i + 128 * c;
+              x[c] = make_float4(gone(id) ? 0.0f : x[c].x, gone(id + 1) ? 0.0f : x[c].y, gone(id + 2) ? 0.0f : x[c].z, gone(id + 3) ? 0.0f : x[c].w);
+            }
+            if (minus) {
+              tv_add(acc[0], tv_term<true>(x[c].x, y[c].x, fa));
+              tv_add(acc[1], tv_term<true>(x[c].y, y[c].y, fa));
+              tv_add(acc[2], tv_term<true>(x[c].z, y[c].z, fa));
+              tv_add(acc[3], tv_term<true>(x[c].w, y[c].w, fa));
+            } else {
+              tv_add(acc[0], tv_term<false>(x[c].x, 0.0f, fa));
+              tv_add(acc[1], tv_term<false>(x[c].y, 0.0f, fa));
+              tv_add(acc[2], tv_term<false>(x[c].z, 0.0f, fa));
+              tv_add(acc[3], tv_term<false>(x[c].w, 0.0f, fa));
+            }
           }
         }
         rs::ff_acc(acc[0], acc[1]);
@@ -283,40 +306,62 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
       if (block == rank) {
         const int w = find(s.warp, TV_WARPS, run, last);
         if (w == warp) {
-          // a contiguous run of the stretch for each lane, the lane that passes, then its ids
-          const int64_t len = hi - lo, each = (len + 31) / 32;
-          const int64_t l0 = min(hi, lo + lane * each), l1 = min(hi, l0 + each);
-          FF mine{0.0f, 0.0f};
-          for (int64_t i = l0; i < l1; ++i)
-            tv_add(mine, minus ? tv_term<true>(pr[i], qr[i], fa) : tv_term<false>(gone(i) ? 0.0f : pr[i], 0.0f, fa));
-          int at = -1, some = -1;
-          FF pre = run, upto = run;
-          for (int k = 0; k < 32; ++k) {
-            const FF v{__shfl_sync(0xFFFFFFFFu, mine.hi, k), __shfl_sync(0xFFFFFFFFu, mine.lo, k)};
-            const FF before = upto;              // what lies in front of that lane's run
-            rs::ff_acc(upto, v);
-            if (__fadd_rn(v.hi, v.lo) > 0.0f && at < 0) {
-              some = k;
-              pre = before;
-              if (!last && rs::ff_diff(upto, target) > 0.0f) at = k;
+          // 128 ids at a time, four of the stretch's vectors on their way together; where the target lies in them, the lane that passes it,
+          // and the id in the lane
+          int64_t pick = -1;                           // last id above 0 so far, in case rounding leaves none
+          bool found = false;
+          for (int64_t i0 = lo; i0 < hi && !found; i0 += 512) {
+            float4 x[4], y[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              x[c] = tv_load<VEC>(pr, i0 + 128 * c + lane * 4, hi);
+              y[c] = minus ? tv_load<VEC>(qr, i0 + 128 * c + lane * 4, hi) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (found) continue;
+              const int64_t id = i0 + 128 * c + lane * 4;
+              const float px[4] = {x[c].x, x[c].y, x[c].z, x[c].w}, qx[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+              FF t[4], mine{0.0f, 0.0f};
+              int top = -1;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                t[e] = minus ? tv_term<true>(px[e], qx[e], fa) : tv_term<false>(id + e < hi && gone(id + e) ? 0.0f : px[e], 0.0f, fa);
+                tv_add(mine, t[e]);
+                if (__fadd_rn(t[e].hi, t[e].lo) > 0.0f) top = e;
+              }
+              FF upto = mine;                          // inclusive over the lanes
+#pragma unroll
+              for (int d = 1; d < 32; d <<= 1) {
+                const FF nb{__shfl_up_sync(0xFFFFFFFFu, upto.hi, d), __shfl_up_sync(0xFFFFFFFFu, upto.lo, d)};
+                if (lane >= d) rs::ff_acc(upto, nb);
+              }
+              FF before{__shfl_up_sync(0xFFFFFFFFu, upto.hi, 1), __shfl_up_sync(0xFFFFFFFFu, upto.lo, 1)};
+              if (lane == 0) before = FF{0.0f, 0.0f};
+              rs::ff_acc(before, run);
+              FF all = upto;
+              rs::ff_acc(all, run);
+              const unsigned past = __ballot_sync(0xFFFFFFFFu, !last && top >= 0 && rs::ff_diff(all, target) > 0.0f);
+              const unsigned some = __ballot_sync(0xFFFFFFFFu, top >= 0);
+              if (past) {
+                const int at = __ffs(int(past)) - 1;
+                int e = top;                           // the lane's last above 0 if rounding leaves none
+                FF sum = before;
+#pragma unroll
+                for (int k = 3; k >= 0; --k) {         // first of the four whose running sum passes
+                  FF s4 = sum;
+                  for (int j = 0; j <= k; ++j) tv_add(s4, t[j]);
+                  if (__fadd_rn(t[k].hi, t[k].lo) > 0.0f && rs::ff_diff(s4, target) > 0.0f) e = k;
+                }
+                pick = __shfl_sync(0xFFFFFFFFu, id + e, at);
+                found = true;
+              } else {
+                if (some) pick = __shfl_sync(0xFFFFFFFFu, id + top, 31 - __clz(int(some)));
+                run = FF{__shfl_sync(0xFFFFFFFFu, all.hi, 31), __shfl_sync(0xFFFFFFFFu, all.lo, 31)};
+              }
             }
           }
-          if (at < 0) {
-            at = some;
-            last = true;
-          }
-          if (lane == at) {
-            int64_t pick = -1;
-            FF sum = pre;
-            for (int64_t i = l0; i < l1; ++i) {
-              const FF t = minus ? tv_term<true>(pr[i], qr[i], fa) : tv_term<false>(gone(i) ? 0.0f : pr[i], 0.0f, fa);
-              if (!(__fadd_rn(t.hi, t.lo) > 0.0f)) continue;
-              pick = i;
-              tv_add(sum, t);
-              if (!last && rs::ff_diff(sum, target) > 0.0f) break;
-            }
-            a.out_tokens[r * T + s.depth] = int32_t(pick);
-          }
+          if (lane == 0) a.out_tokens[r * T + s.depth] = int32_t(pick);
         }
       }
       break;
@@ -369,9 +414,9 @@ extern "C" dspark_status dspark_tree_verify(const float* p, int64_t ldp, const f
   if (R == 0) return DSPARK_OK;
   DS_REQUIRE(p && tokens && u_accept && u_draw && out_tokens && n_accepted && path && dev_status);
   DS_REQUIRE(ds_aligned(p, 4) && ds_aligned(q, 4) && ds_aligned(u_accept, 8) && ds_aligned(u_draw, 8));
-  // blocks for a request: as many as one wave of four blocks an SM holds
+  // blocks for a request: as many as one wave of two blocks an SM holds
   int ranks = TV_MAXC;
-  while (ranks > 1 && R * ranks > 4 * int64_t(ds_num_sms())) ranks >>= 1;
+  while (ranks > 1 && R * ranks > 2 * int64_t(ds_num_sms())) ranks >>= 1;
   TvArgs a{p, q, ldp, ldq, V, tokens, parent, n_nodes, u_accept, u_draw, T, 0, out_tokens, n_accepted, path, dev_status};
   a.seg = ds_ceil_div(ds_ceil_div(V, int64_t(ranks) * TV_WARPS), 4) * 4;
   const bool vec = ds_aligned(p, 16) && ldp % 4 == 0 && (!q || (ds_aligned(q, 16) && ldq % 4 == 0));
