@@ -119,7 +119,7 @@ DS_DEV void qa_turn(const T* head, int d, int rot, bool interleaved, const float
 // magnitude by shuffles, so a column is loaded once and its code needs no second pass. Every byte moves once: bound by HBM for many
 // rows, by the latency of the lookups for few (with few rows grid.y splits the items of a row).
 template <typename T, int VEC, int NR>
-__global__ void __launch_bounds__(QA_THREADS) rope_append_q8_kernel(const QaArgs a) {
+__global__ void __launch_bounds__(QA_THREADS, NR > 1 ? 14 : 1) rope_append_q8_kernel(const QaArgs a) {
   constexpr int GROUP = Q8_BLOCK / VEC;                // threads of a block of columns
   __shared__ __align__(16) float s_cs[NR][256];
   __shared__ Q8Slot s_slot[NR];                        // at >= 0; -1 a slot without a place; -2 not a node
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(QA_THREADS) rope_append_q8_kernel(const QaArgs
     }
   }
   // keys, then values: the block's threads stay together for the shuffles
-  bool odd = false;                                    // a number that is not finite was among them
+  bool odd = false;                                    // a number that is not finite was among a block's
   const int heads = rows * 2 * Hk;                     // per row: keys' heads, values' heads
   QaItem it(first, per, step);
   for (int u0 = first - tid; u0 < heads * per; u0 += step, it.next()) {
@@ -242,17 +242,25 @@ __global__ void __launch_bounds__(QA_THREADS) rope_append_q8_kernel(const QaArgs
       qa_load<T, VEC>(src + d, y);
       if (!value) qa_turn<T, VEC>(src, d, a.rot, a.interleaved != 0, s_cs[m], y);
     }
-    float most = 0.0f;
+    // largest magnitude of the block, as bits, which compare as numbers do; what is not finite lies above all that is
+    uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const bool finite = fabsf(y[e]) < INFINITY;
-      odd = odd || !finite;
-      most = fmaxf(most, finite ? fabsf(y[e]) : 0.0f);
+    for (int e = 0; e < VEC; ++e) top = max(top, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 1; o < GROUP; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (__any_sync(0xFFFFFFFFu, top >= 0x7F800000u)) {
+      odd = odd || top >= 0x7F800000u;
+      top = 0;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        if (y[e] != y[e]) y[e] = 0.0f;
+        if (fabsf(y[e]) < INFINITY) top = max(top, __float_as_uint(fabsf(y[e])));
+      }
+#pragma unroll
+      for (int o = 1; o < GROUP; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     }
-#pragma unroll
-    for (int o = 1; o < GROUP; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
     if (!there || at.at < 0) continue;
-    const uint32_t byte = q8_choose(most, e4m3);
+    const uint32_t byte = q8_choose(__uint_as_float(top), e4m3);
     const float inv = __uint_as_float((254u - byte) << 23);
     uint8_t* dst = reinterpret_cast<uint8_t*>(value ? a.c.v : a.c.k) + at.at + int64_t(hd) * a.c.head_stride + d;
     if constexpr (VEC == 8) {

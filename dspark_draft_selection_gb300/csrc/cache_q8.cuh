@@ -31,12 +31,10 @@ DS_DEV uint32_t q8_choose(float m, bool e4m3) {
   return uint32_t(min(max(e, -126), 118) + 127);
 }
 
-// Codes of four numbers under 2^-e (`inv`), the first in the low byte. Infinities become the largest code, what is not a number 0. E4M3: the
+// Codes of four numbers under 2^-e (`inv`), the first in the low byte; infinities become the largest code. E4M3: the
 // conversion rounds to nearest, ties to even, and saturates. INT8: adding 1.5 * 2^23 leaves the rounded number in the low bits.
 DS_DEV uint32_t q8_codes(float y0, float y1, float y2, float y3, float inv, bool e4m3) {
-  float z[4] = {y0 * inv, y1 * inv, y2 * inv, y3 * inv};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) z[e] = z[e] == z[e] ? z[e] : 0.0f;
+  const float z[4] = {y0 * inv, y1 * inv, y2 * inv, y3 * inv};
   if (e4m3) {
     uint16_t lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(z[1]), "f"(z[0]));
