@@ -32,6 +32,7 @@ struct TvShared {
   int32_t par[TV_MAXT], tok[TV_MAXT], first[TV_MAXT], next[TV_MAXT], path[TV_MAXT], dup[TV_MAXT];
   float px[TV_MAXT], qx[TV_MAXT];
   FF warp[TV_WARPS], part[2][TV_MAXC];       // stretches of this block; shares of all blocks, two rounds of them
+  uint32_t filter[64];                       // a bit for every refused id modulo 2048 (q absent)
   FF a;
   int32_t cur, done, refused, depth;         // row asked for; whether the walk ended; first refused child (q absent), depth
 };
@@ -192,6 +193,13 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
       __syncthreads();
       const bool done = s.done != 0;
       const FF fa = s.a;
+      if constexpr (!Q) {                              // only the draw's sum leaves ids out: the walk has ended
+        if (tid < 64) s.filter[tid] = 0u;
+        __syncthreads();
+        for (int k = tid; k < n; k += TV_THREADS)
+          if (!plain && s.par[k] == s.cur && s.tok[k] >= 0) atomicOr(&s.filter[(s.tok[k] >> 5) & 63], 1u << (s.tok[k] & 31));
+        __syncthreads();
+      }
       const bool known = done && Q && round > 0 && !plain && fa.hi != 0.0f;     // the row's sum is the last one
       const int64_t row = r * T + s.cur;
       const float* pr = a.p + row * a.ldp;
@@ -202,6 +210,7 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
       // refused children of this node, without q: their ids count as 0
       auto gone = [&](int64_t id) {
         if constexpr (!Q) {
+          if (((s.filter[(id >> 5) & 63] >> (id & 31)) & 1u) == 0u) return false;
           for (int k = plain ? TV_MAXT : s.refused; k < TV_MAXT; k = s.next[k])
             if (s.tok[k] == id) return true;
         }

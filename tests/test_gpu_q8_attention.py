@@ -235,3 +235,62 @@ def test_many_requests_and_strided_queries():
     ctx = rng.integers(0, 90, R).tolist()
     c = Q8Case(R, 2, 4, 2, 64, 16, ctx, None, "bf16", "e4m3", mask="chain").run()
     c.check()
+
+
+@pytest.mark.parametrize("T", [1, 8, 40])
+def test_pages_past_two_to_the_31_bytes(T):
+    """Codes and scales whose offsets pass 32 bits."""
+    H, D, page = 8, 128, 64
+    pages = 2 ** 31 // (page * H * D) + 40
+    codes = [torch.empty((pages, page, H, D), dtype=torch.uint8, device="cuda").view(torch.int8) for _ in range(2)]
+    wide = [torch.empty((pages, H, 16, page, 4), dtype=torch.uint8, device="cuda")[:, :, 3].transpose(1, 2) for _ in range(2)]
+    c = Q8Case(T, T, 16, H, D, page, [150], None, "bf16", "int8", mask="chain")
+    far = torch.tensor([[pages - 1, pages - 30, 3]], dtype=torch.int32, device="cuda")
+    big = (*codes, *wide)
+    for b, small in zip(big, c.cache):
+        for e in range(far.shape[1]):
+            b[int(far[0, e])] = small[int(c.table[0, e])]
+    c.run()
+    want = c.out.clone()
+    c.cache, c.table = big, far
+    c.run()
+    assert int(c.status) == 0 and torch.equal(c.out, want)
+
+
+@pytest.mark.parametrize("T", [1, 6, 40, 90])
+def test_a_wait_that_runs_out_is_reported(T):
+    import dspark_draft_selection_gb300 as ds
+    c = Q8Case(T, T, 8, 2, 128, 64, [2000], None)
+    try:
+        ds.dspark_test_set_first_wait_polls(0)
+        c.run()
+        assert int(c.status) == 6
+    finally:
+        ds.dspark_test_set_first_wait_polls(0xFFFFFFFF)
+    c.run().check(rows=[0, T - 1])
+
+
+def test_refusals():
+    import dspark_draft_selection_gb300 as ds
+    c = Q8Case(4, 4, 4, 2, 64, 16, [50], None)
+    ctx = torch.tensor([50], dtype=torch.int32, device="cuda")
+    call = lambda **o: ds.dspark_tree_attention_q8(**{**dict(q=c.q, cache=c.cache, page_table=c.table, ctx_len=ctx, mask=c.mask), **o})  # noqa: E731
+    assert call()[0].shape == c.q.shape
+    for bad in (dict(scale=0.0), dict(scale=float("nan")), dict(softcap=-1.0), dict(softcap=float("inf")), dict(q=c.q[:, :, :3]),
+                dict(ws=torch.empty(1000, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ds.DsparkError):
+            call(**bad)
+    for bad in (dict(mask=c.mask[:, :, :0]), dict(mask=c.mask.long()), dict(ctx_len=ctx.long()), dict(q=c.q.transpose(1, 2)),
+                dict(lse=torch.empty((1, 4), device="cuda")), dict(q=c.q[..., :32]), dict(n_nodes=torch.zeros(2, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    with pytest.raises(TypeError):
+        call(q=c.q.half())
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    import dspark_draft_selection_gb300 as ds
+    c = Q8Case(1, 1, 4, 2, 64, 16, [50], None).run()
+    monkeypatch.setattr(ds._binding, "_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        c.run()
