@@ -638,19 +638,19 @@ def q8_cache(pages, page, heads, head_dim, *, layers=None, dtype=torch.float8_e4
     return (*codes, *scales)
 
 
-def _here(*tensors):
-    """The kernels run on the current device: tensors of another are refused."""
-    here = _device()
-    for t in tensors:
-        if here is not None and t is not None and t.is_cuda and t.device.index != here:
-            raise ValueError(f"a tensor of {t.device}, but the current device is cuda:{here}: call within torch.cuda.device({t.device.index})")
+def _here(t):
+    """The kernels run on the current device: a tensor of another is refused."""
+    if t.is_cuda:
+        here = _device()
+        if here is not None and t.get_device() != here:
+            raise ValueError(f"a tensor of {t.device}, but the current device is cuda:{here}: call within torch.cuda.device({t.get_device()})")
 
 
 def _qcache(cache, page_table):
     """(bytes of a dspark_qcache, heads, head_dim, requests) of cache = (k, v, k_scale, v_scale) as q8_cache makes it (any strides, the
     last 1) and page_table [R, n]."""
     k, v, ks, vs = cache
-    _here(k, v, ks, vs, page_table)
+    _here(k)
     sh, st, ssh, sst = k.shape, k.stride(), ks.shape, ks.stride()
     if v.shape != sh or v.stride() != st or v.dtype is not k.dtype:
         raise ValueError("keys and values are of one shape, layout and type")
@@ -784,7 +784,7 @@ def dspark_tree_verify(p, tokens, parent, u_accept, u_draw, *, q=None, n_nodes=N
     status) as dspark_tree_accept does."""
     if stream is not None:
         return _on(stream, dspark_tree_verify, locals())
-    _here(p, q, tokens)
+    _here(p)
     R, T = tokens.shape
     V = p.shape[-1]
     dev = tokens.device

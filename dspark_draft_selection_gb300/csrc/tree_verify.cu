@@ -34,7 +34,7 @@ struct TvShared {
   FF warp[TV_WARPS], part[2][TV_MAXC];       // stretches of this block; shares of all blocks, two rounds of them
   uint32_t filter[64];                       // a bit for every refused id modulo 2048 (q absent)
   FF a;
-  int32_t cur, done, refused, depth;         // row asked for; whether the walk ended; first refused child (q absent), depth
+  int32_t cur, done, known, refused, depth;  // row asked for; whether the walk ended, and its sum is known; first refused child (q absent), depth
 };
 
 DS_DEV FF tv_pair(double x) {
@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
   // thread 0's state of the walk
   int cur = 0, child = 0, depth = 0;
   double da = 0.0, db = 1.0;
+  bool open = false;                                   // b of this a is not known yet; db is the one before
   if (tid == 0 && n > 0) {
     s.path[0] = 0;
     child = s.first[0];
@@ -153,8 +154,9 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
     for (;;) {
       if (tid == 0) {
         int done = 0;
-        if (round > 0 && Q && !plain && !s.done) {        // the sum that the last refusal asked for
+        if (open && round > 0 && !plain) {             // the sum that the test of `child` asked for
           db = rs::ff_value(total);
+          open = false;
         }
         for (;;) {
           if (child >= TV_MAXT || plain) {
@@ -162,33 +164,40 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
             break;
           }
           const int x = child;
-          child = s.next[x];
           const int32_t tok = s.tok[x];
           if (tok < 0) {
             ds_set_error(a.status, DSPARK_ERANGE);
+            child = s.next[x];
             continue;
           }
           const double px = double(s.px[x]), u = a.ua[r * T + x];
           const double left = Q ? fmax(0.0, px - da * double(s.qx[x])) : (s.dup[x] ? 0.0 : px);
-          if (u * db * (Q ? double(s.qx[x]) : 1.0) < left) {
+          // While b is not known it is at most the one before (a hair more, where p does not quite sum to 1): a child that would be accepted
+          // with that one needs no sum.
+          if (u * (open ? db * 1.0001 : db) * (Q ? double(s.qx[x]) : 1.0) < left) {
             cur = x;
             s.path[++depth] = x;
             child = s.first[x];
             da = 0.0;
             db = 1.0;
+            open = false;
             continue;
           }
+          if (open) break;                             // the others are needed for b
+          child = s.next[x];
           if (Q) {
             da += db;
-            break;                                     // the others are needed for b
+            open = true;
+          } else {
+            db -= left;
           }
-          db -= left;
         }
         s.cur = cur;
         s.done = done;
         s.depth = depth;
         s.refused = s.first[cur];
         s.a = tv_pair(da);
+        s.known = Q && !open && !plain && da != 0.0;
       }
       __syncthreads();
       const bool done = s.done != 0;
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
           if (!plain && s.par[k] == s.cur && s.tok[k] >= 0) atomicOr(&s.filter[(s.tok[k] >> 5) & 63], 1u << (s.tok[k] & 31));
         __syncthreads();
       }
-      const bool known = done && Q && round > 0 && !plain && fa.hi != 0.0f;     // the row's sum is the last one
+      const bool known = done && s.known != 0;         // the row's sum is the last one
       const int64_t row = r * T + s.cur;
       const float* pr = a.p + row * a.ldp;
       const float* qr = Q ? a.q + row * a.ldq : nullptr;
