@@ -13,8 +13,6 @@ namespace {
 using rs::FF;
 
 constexpr int TV_MAXT = 512;
-constexpr int TV_THREADS = 512;
-constexpr int TV_WARPS = TV_THREADS / 32;
 constexpr int TV_MAXC = 8;                   // blocks of a cluster
 
 struct TvArgs {
@@ -28,10 +26,11 @@ struct TvArgs {
 };
 
 // A block's share of what the whole cluster adds up, and what thread 0 asks of the others.
+template <int WARPS>
 struct TvShared {
   int32_t par[TV_MAXT], tok[TV_MAXT], first[TV_MAXT], next[TV_MAXT], path[TV_MAXT], dup[TV_MAXT];
   float px[TV_MAXT], qx[TV_MAXT];
-  FF warp[TV_WARPS], part[2][TV_MAXC];       // stretches of this block; shares of all blocks, two rounds of them
+  FF warp[WARPS], part[2][TV_MAXC];       // stretches of this block; shares of all blocks, two rounds of them
   uint32_t filter[64];                       // a bit for every refused id modulo 2048 (q absent)
   FF a;
   int32_t cur, done, known, refused, depth;  // row asked for; whether the walk ended, and its sum is known; first refused child (q absent), depth
@@ -90,9 +89,10 @@ DS_DEV int tv_ranks() {
 // a row, each warp of the cluster taking one stretch of it. The stretches' sums then also say where the draw's target lies: the warp whose
 // stretch holds it reads it once more. Sums are float pairs, 2Sum and FMA, 48 bits: a token is drawn where a sum passes a border, and with
 // 10^5 ids a float32 sum would put one draw in a hundred on the other side.
-template <bool Q, int VEC>
-__global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a) {
-  __shared__ TvShared s;
+template <bool Q, int VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) tree_verify_kernel(const TvArgs a) {
+  constexpr int WARPS = THREADS / 32;
+  __shared__ TvShared<WARPS> s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = tv_rank(), ranks = tv_ranks();
   const int64_t r = blockIdx.x / uint32_t(ranks);
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
     if (tid == 0) ds_set_error(a.status, DSPARK_EINVAL);
     n = 0;
   }
-  for (int i = tid; i < T; i += TV_THREADS) {
+  for (int i = tid; i < T; i += THREADS) {
     int32_t par = -1, tok = -1;
     if (i > 0 && i < n) {
       par = a.parent ? a.parent[r * T + i] : i - 1;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
     s.qx[i] = Q && par >= 0 && tok >= 0 ? a.q[(r * T + par) * a.ldq + tok] : 1.0f;
   }
   __syncthreads();
-  for (int i = tid; i < n; i += TV_THREADS) {
+  for (int i = tid; i < n; i += THREADS) {
     const int32_t par = s.par[i], tok = s.tok[i];
     if (par < 0) continue;
     atomicMin(&s.first[par], i);
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
       if constexpr (!Q) {                              // only the draw's sum leaves ids out: the walk has ended
         if (tid < 64) s.filter[tid] = 0u;
         __syncthreads();
-        for (int k = tid; k < n; k += TV_THREADS)
+        for (int k = tid; k < n; k += THREADS)
           if (!plain && s.par[k] == s.cur && s.tok[k] >= 0) atomicOr(&s.filter[(s.tok[k] >> 5) & 63], 1u << (s.tok[k] & 31));
         __syncthreads();
       }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
       const int64_t row = r * T + s.cur;
       const float* pr = a.p + row * a.ldp;
       const float* qr = Q ? a.q + row * a.ldq : nullptr;
-      lo = min(a.V, (int64_t(rank) * TV_WARPS + warp) * a.seg);
+      lo = min(a.V, (int64_t(rank) * WARPS + warp) * a.seg);
       hi = min(a.V, lo + a.seg);
       const bool minus = Q && (fa.hi != 0.0f || fa.lo != 0.0f) && !plain;
       // refused children of this node, without q: their ids count as 0
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
         __syncthreads();
         if (tid < ranks) {
           FF sum = s.warp[0];
-          for (int k = 1; k < TV_WARPS; ++k) rs::ff_acc(sum, s.warp[k]);
+          for (int k = 1; k < WARPS; ++k) rs::ff_acc(sum, s.warp[k]);
           if (ranks > 1) tv_put_remote(&s.part[round & 1][rank], tid, sum);
           else s.part[round & 1][0] = sum;
         }
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
       bool last = false;
       const int block = find(part, ranks, run, last);
       if (block == rank) {
-        const int w = find(s.warp, TV_WARPS, run, last);
+        const int w = find(s.warp, WARPS, run, last);
         if (w == warp) {
           // 128 ids at a time, four of the stretch's vectors on their way together; where the target lies in them, the lane that passes it,
           // and the id in the lane
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
     __syncthreads();
     const int depth_ = n > 0 ? s.depth : -1;
     if (tid == 0) a.n_accepted[r] = depth_;
-    for (int i = tid; i < T; i += TV_THREADS) {
+    for (int i = tid; i < T; i += THREADS) {
       a.path[r * T + i] = i <= depth_ ? s.path[i] : -1;
       if (i != depth_ || n == 0) a.out_tokens[r * T + i] = i < depth_ ? s.tok[s.path[i + 1]] : -1;
     }
@@ -398,11 +398,11 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const TvArgs a)
   if (ranks > 1) tv_cluster_sync();
 }
 
-template <bool Q, int VEC>
+template <bool Q, int VEC, int THREADS>
 cudaError_t tv_launch(const TvArgs& a, int64_t R, int ranks, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(R * ranks));
-  cfg.blockDim = dim3(TV_THREADS);
+  cfg.blockDim = dim3(THREADS);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -413,12 +413,13 @@ cudaError_t tv_launch(const TvArgs& a, int64_t R, int ranks, cudaStream_t st) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, tree_verify_kernel<Q, VEC>, a);
+  return cudaLaunchKernelEx(&cfg, tree_verify_kernel<Q, VEC, THREADS>, a);
 }
 
+template <int THREADS>
 cudaError_t tv_dispatch(const TvArgs& a, int64_t R, int ranks, bool vec, cudaStream_t st) {
-  if (a.q) return vec ? tv_launch<true, 4>(a, R, ranks, st) : tv_launch<true, 1>(a, R, ranks, st);
-  return vec ? tv_launch<false, 4>(a, R, ranks, st) : tv_launch<false, 1>(a, R, ranks, st);
+  if (a.q) return vec ? tv_launch<true, 4, THREADS>(a, R, ranks, st) : tv_launch<true, 1, THREADS>(a, R, ranks, st);
+  return vec ? tv_launch<false, 4, THREADS>(a, R, ranks, st) : tv_launch<false, 1, THREADS>(a, R, ranks, st);
 }
 
 }  // namespace
@@ -432,12 +433,15 @@ extern "C" dspark_status dspark_tree_verify(const float* p, int64_t ldp, const f
   if (R == 0) return DSPARK_OK;
   DS_REQUIRE(p && tokens && u_accept && u_draw && out_tokens && n_accepted && path && dev_status);
   DS_REQUIRE(ds_aligned(p, 4) && ds_aligned(q, 4) && ds_aligned(u_accept, 8) && ds_aligned(u_draw, 8));
-  // blocks for a request: as many as one wave of two blocks an SM holds
+  // Blocks for a request: as many as one wave of 1,024 threads an SM holds. With more requests than eight blocks of 512 threads each let into a
+  // wave, blocks have 256 threads: 64 trees of 24 nodes 52 us, with 512 threads 60 us; one tree 17 us with 512 threads, 21 us with 256.
+  const int64_t sms = ds_num_sms();
+  const int threads = R * TV_MAXC > 2 * sms ? 256 : 512;
   int ranks = TV_MAXC;
-  while (ranks > 1 && R * ranks > 2 * int64_t(ds_num_sms())) ranks >>= 1;
+  while (ranks > 1 && R * ranks > 1024 / threads * sms) ranks >>= 1;
   TvArgs a{p, q, ldp, ldq, V, tokens, parent, n_nodes, u_accept, u_draw, T, 0, out_tokens, n_accepted, path, dev_status};
-  a.seg = ds_ceil_div(ds_ceil_div(V, int64_t(ranks) * TV_WARPS), 4) * 4;
+  a.seg = ds_ceil_div(ds_ceil_div(V, int64_t(ranks) * (threads / 32)), 4) * 4;
   const bool vec = ds_aligned(p, 16) && ldp % 4 == 0 && (!q || (ds_aligned(q, 16) && ldq % 4 == 0));
-  DS_CUDA_TRY(tv_dispatch(a, R, ranks, vec, stream));
+  DS_CUDA_TRY(threads == 512 ? tv_dispatch<512>(a, R, ranks, vec, stream) : tv_dispatch<256>(a, R, ranks, vec, stream));
   return DSPARK_OK;
 }
