@@ -14,8 +14,8 @@ constexpr int QA_MAXROWS = 2;
 constexpr int QC_THREADS = 128;
 constexpr int QC_MAXT = 512;
 constexpr int QC_BATCH = 8;
-constexpr int QR_THREADS = 256;
-constexpr int QR_ROWS = 16;
+constexpr int QR_THREADS = 128;
+constexpr int QR_ROWS = 8;
 
 struct QaArgs {
   const void *q, *k, *v;
@@ -116,8 +116,9 @@ DS_DEV void qa_turn(const T* head, int d, int rot, bool interleaved, const float
 
 // One or two node slots a block: their cosines and sines are staged in shared memory once for all heads, then the threads go over
 // the heads' items of VEC columns: queries, keys, values. The 32 / VEC neighbouring threads that hold a block of 32 columns find its largest
-// magnitude by shuffles, so a column is loaded once and its code needs no second pass. Every byte moves once: bound by HBM for many
-// rows, by the latency of the lookups for few (with few rows grid.y splits the items of a row).
+// magnitude by shuffles, so a column is loaded once and its code needs no second pass. Every byte moves once. 15,000 rows of 32 + 2 x 8 heads of 128
+// in bf16: 68 us, 4.6 TB/s; the queries' part of it runs at the rate of HBM, the keys' and values' part (39 us of them) is bound by the instructions of
+// rotation, magnitude and conversion. Few rows are bound by the latency of the lookups: 8 rows 3 us of the GPU.
 template <typename T, int VEC, int NR>
 __global__ void __launch_bounds__(QA_THREADS, NR > 1 ? 14 : 1) rope_append_q8_kernel(const QaArgs a) {
   constexpr int GROUP = Q8_BLOCK / VEC;                // threads of a block of columns
@@ -275,6 +276,8 @@ __global__ void __launch_bounds__(QA_THREADS, NR > 1 ? 14 : 1) rope_append_q8_ke
 
 template <typename T, int VEC>
 cudaError_t qa_launch(const QaArgs& a, cudaStream_t st) {
+  // Two rows a block from twelve blocks an SM on: 15,000 rows 68 us, with one row each 95 us; 2,500 rows 22.1 and 23.7 us, but 1,500 rows 17.0 and
+  // 15.9 us, 64 rows 16.5 and 14.8 us. With fewer rows than SMs a row's items are split over blocks (8 rows 15.0 us, unsplit 15.8 us, both with the call).
   const int64_t sms = ds_num_sms();
   if (a.rows >= sms * 12)
     return ds_launch(rope_append_q8_kernel<T, VEC, QA_MAXROWS>, dim3(unsigned(ds_ceil_div(a.rows, QA_MAXROWS))), dim3(QA_THREADS), 0, st, a);
@@ -289,13 +292,14 @@ cudaError_t qa_dispatch(const QaArgs& a, cudaStream_t st) {
   const bool vec = ds_aligned(a.q, 16) && ds_aligned(a.k, 16) && ds_aligned(a.v, 16) && ds_aligned(a.q_out, 16) &&
                    (a.ldq * e) % 16 == 0 && (a.ldk * e) % 16 == 0 && (a.ldv * e) % 16 == 0 && (a.ldo * e) % 16 == 0 &&
                    q8_codes_aligned(&a.c, 8) && (a.interleaved ? a.rot : a.rot / 2) % 8 == 0;
-  return vec ? qa_launch<T, 8>(a, st) : qa_launch<T, 1>(a, st);
+  return vec ? qa_launch<T, 8>(a, st) : qa_launch<T, 1>(a, st);      // 15,000 rows 68 us, a column at a time 236 us
 }
 
 // --- commit ---
 // grid (layer x {K, V}, request): a block moves one buffer's codes and scales of one layer of one request. Sources lie above their
 // destinations and both rise, so a thread that reads QC_BATCH rows of its column before it writes them, batch after batch, never
-// overwrites a row that it still has to read; rows that stay where they are are dropped first. Each moved byte is read and written once.
+// overwrites a row that it still has to read; rows that stay where they are are dropped first. Each moved byte is read and written once. Bound by
+// the chain path, page, codes: 64 requests of 16 layers 10.2 us with 16 bytes and 4 scales at a time, 11.2 us with 8 bytes and one scale.
 template <int VC, int VS>
 __global__ void __launch_bounds__(QC_THREADS) cache_commit_q8_kernel(const dspark_qcache c, const int32_t* ctx_len, const int32_t* path,
                                                                      const int32_t* n_accepted, int32_t T_, int32_t* new_len,
@@ -383,8 +387,22 @@ struct QrArgs {
   int32_t* status;
 };
 
+// Four E4M3 codes, through f16, which holds them all.
+DS_DEV float4 qr_e4m3(uint32_t w) {
+  float4 z;
+  asm("{\n\t.reg .b16 l, h, a, b, c, d;\n\t.reg .b32 x, y;\n\tmov.b32 {l, h}, %4;\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, l;\n\tcvt.rn.f16x2.e4m3x2 y, h;\n\tmov.b32 {a, b}, x;\n\tmov.b32 {c, d}, y;\n\t"
+      "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\tcvt.f32.f16 %2, c;\n\tcvt.f32.f16 %3, d;\n\t}"
+      : "=f"(z.x), "=f"(z.y), "=f"(z.z), "=f"(z.w)
+      : "r"(w));
+  return z;
+}
+
 // A block reads QR_ROWS slots: their places are looked up once, then the threads go over the slots' heads (keys, then values) VEC codes at a
-// time, side by side. Bound by HBM: 1 + 1/32 bytes read and 2 or 4 written a column.
+// time, side by side. Bound by HBM: 1 + 1/32 bytes read and 2 or 4 written a column. 136,000 slots of 8 heads of 128 to bf16: 141 us, 6.0 TB/s.
+// Few loads a thread and small blocks are best, as reads and writes then alternate least far apart: 16 slots and 256 threads a block with four
+// loads a thread 167 us, with two 148 us; 8 slots, 128 threads and two loads 141 us; one load 157 us. A number times its scale is exact in
+// float32, and in bf16 too (eight bits of fraction hold every code).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(QR_THREADS) cache_read_q8_kernel(const QrArgs a) {
   __shared__ Q8Slot s_slot[QR_ROWS];                   // at -1: a slot without a place; -2: a row that is left as it is
@@ -414,8 +432,7 @@ __global__ void __launch_bounds__(QR_THREADS) cache_read_q8_kernel(const QrArgs 
   const bool e4m3 = a.c.code == DSPARK_E4M3;
   int m = tid / items, x = tid - m * items;            // slot of the block, item of the slot
   while (m < QR_ROWS) {
-    // four items' codes on their way together
-    constexpr int AT = 4;
+    constexpr int AT = 2;                              // items whose codes are on their way together
     uint4 w[AT];
     float f[AT];
     T* to[AT];
@@ -456,7 +473,14 @@ __global__ void __launch_bounds__(QR_THREADS) cache_read_q8_kernel(const QrArgs 
         for (int u = 0; u < VEC / 8; ++u) {
           float y[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = q8_number((u ? (e < 4 ? w[c].z : w[c].w) : (e < 4 ? w[c].x : w[c].y)) >> (8 * (e & 3)), e4m3) * f[c];
+          for (int e = 0; e < 8; e += 4) {
+            const uint32_t w4 = u ? (e ? w[c].w : w[c].z) : (e ? w[c].y : w[c].x);
+            const float4 z = e4m3 ? qr_e4m3(w4) : make_float4(float(int8_t(w4)), float(int8_t(w4 >> 8)), float(int8_t(w4 >> 16)), float(int8_t(w4 >> 24)));
+            y[e] = z.x * f[c];
+            y[e + 1] = z.y * f[c];
+            y[e + 2] = z.z * f[c];
+            y[e + 3] = z.w * f[c];
+          }
           qa_store<T, 8>(to[c] + 8 * u, y);
         }
       }
@@ -514,12 +538,14 @@ extern "C" dspark_status dspark_cache_read_q8(const dspark_qcache* cache, const 
   a.c.layer_stride = a.c.scale_layer_stride = 0;
   const bool vec = q8_codes_aligned(&a.c, 8) && ds_aligned(k_out, 16) && ds_aligned(v_out, 16) && (ld * int64_t(e)) % 16 == 0;
   const dim3 grid(unsigned(ds_ceil_div(a.rows, QR_ROWS)));
-  const bool v16 = vec && cache->head_dim % 16 == 0 && q8_codes_aligned(&a.c, 16);
+  // Codes a load: 16 for bf16 rows (136,000 slots 141 us; 8 at a time 208 us), 8 for float32 rows (272 us; 16 at a time, whose stores lie 64 bytes
+  // apart, 292 us), one where rows are not aligned for that.
+  const bool v16 = vec && dtype == DSPARK_BF16 && cache->head_dim % 16 == 0 && q8_codes_aligned(&a.c, 16);
   auto go = [&](auto kern) { return ds_launch(kern, grid, dim3(QR_THREADS), 0, stream, a); };
   if (dtype == DSPARK_BF16) {
     DS_CUDA_TRY((v16 ? go(cache_read_q8_kernel<__nv_bfloat16, 16>) : vec ? go(cache_read_q8_kernel<__nv_bfloat16, 8>) : go(cache_read_q8_kernel<__nv_bfloat16, 1>)));
   } else {
-    DS_CUDA_TRY((v16 ? go(cache_read_q8_kernel<float, 16>) : vec ? go(cache_read_q8_kernel<float, 8>) : go(cache_read_q8_kernel<float, 1>)));
+    DS_CUDA_TRY(vec ? go(cache_read_q8_kernel<float, 8>) : go(cache_read_q8_kernel<float, 1>));
   }
   return DSPARK_OK;
 }

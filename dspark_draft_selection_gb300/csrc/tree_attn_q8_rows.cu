@@ -20,6 +20,13 @@
 // Every warp copies its own slices with TMA, NS of them in flight, and waits for nothing but its own barriers. The work is the line of
 // tiles of tree_attn.cuh with 16 keys a tile: a block's share is cut once more into its warps' shares; what two warps leave of an item is joined
 // at the end in shared memory (in the order of the keys), and what two blocks leave by the join kernel.
+//
+// Bound by HBM (2 (D + D / 32) bytes a key and key head) for 4 rows a key head, by the latency of a warp's chain of scores, weights and
+// products for more (with 17 to 32 rows 255 registers a thread leave 8 warps an SM). Measured with the join, 300-8,200 keys, heads of 128, 8 of them:
+//   64 requests of one token x 4 heads    127 us   4.6 TB/s, 0.68 of the measured copy rate (with a bf16 cache 188 us)
+//   32 requests of 4 nodes x 4 heads      103 us
+//   32 requests of 8 nodes x 4 heads      189 us   (with a bf16 cache 114 us, whose kernel reads tiles as they lie)
+//   one token x 4 heads, 5,001 keys        19 us   with the host's call: two slices a warp, then the joins
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -36,6 +43,7 @@ constexpr float TQ_NONE = -3e38f;            // reference of a row that has seen
 
 template <int DP, int NQ>
 struct TqLayout {
+  // 12 warps of 168 registers, or 8 of 255 where four tiles need them. (One tile with 8 or with 16 warps of fewer registers was slower.)
   static constexpr int WARPS = NQ <= 2 ? 12 : 8;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int NS = NQ == 1 ? 3 : NQ == 2 ? 2 : 4;

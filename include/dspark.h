@@ -601,7 +601,7 @@ dspark_status dspark_cache_read_q8(const dspark_qcache* cache, const int32_t* st
 /*
  * Sampled acceptance along a tree from given random numbers (dspark_verify does it for chains from logits and seeds).
  * p: [R * T, ldp] float32 device, V columns: row r * T + i is the target's distribution after node i (with whatever filters the
- * caller applies; its entries are finite and >= 0 and sum to 1). q: NULL, or rows of the same form ([R * T, ldq]): row r * T + i is the
+ * caller applies; its entries are finite and >= 0 and sum to 1 within 1/100). q: NULL, or rows of the same form ([R * T, ldq]): row r * T + i is the
  * distribution that node i's children were drawn from, independently of each other. NULL: the children were not drawn (the best
  * candidates, say) and count as certain. tokens, parent (NULL: chains), n_nodes as in dspark_tree_accept; u_accept [R, T] and u_draw [R]
  * float64 device, in [0, 1).
