@@ -73,6 +73,16 @@ def test_trees(R, T, V, pad, drawn):
     Trees(R + T + V, R, T, V, drawn, pad=pad).check()
 
 
+@pytest.mark.parametrize("total", [0.992, 1.008])
+@pytest.mark.parametrize("V", [7, 3001])
+def test_rows_that_were_rounded(V, total):
+    """Rows that sum to 1 within 1/100 only, with proposals that have little in common with them, so that a residual keeps nearly all of a
+    row's mass and many siblings are tested against it."""
+    t = Trees(V, 40, 24, V, True, back=2, near=6.0)
+    t.p = (t.p * np.float32(total)).astype(np.float32)
+    t.check()
+
+
 @pytest.mark.parametrize("drawn", [False, True])
 def test_full_vocabulary(drawn):
     Trees(3, 2, 6, 151936, drawn).check()
