@@ -65,8 +65,8 @@ extern "C" dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, ds
   };
   DS_REQUIRE(counts(64));
   // Few rows a key head: the kernel that widens codes in operand registers; more: the one that stages them for tcgen05, which takes the same
-  // time whatever the rows up to 128. 300-8,200 keys: 64 requests with 4 rows 127 and 383 us; 32 requests with 16 rows 103 and 205 us, with 32 rows 189 and
-  // 202 us (the first would take twice as many registers for more).
+  // time whatever the rows up to 128. 300-8,200 keys: 64 requests with 4 rows 127 and 383 us; 32 requests with 16 rows 103 and 195 us, with 32 rows 187 and
+  // 185 us, but 197 and more than 270 us where scales lie by place and not by head.
   const bool few = a.rows <= 32;
   int box = few ? 16 : 128;
   while (cache->page_size % box) box >>= 1;
@@ -79,7 +79,7 @@ extern "C" dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, ds
   const bool maps = tc && tq_tensor_map(&mk, cache->k, *cache, cols, box) && tq_tensor_map(&mv, cache->v, *cache, cols, box);
   a.box = box;
   const int nb = q8_blocks(int(D));
-  // Scale bytes of a tile by bulk copies where a box's lie side by side: 4 capped trees of 64 nodes 358 us, by plain loads 477 us.
+  // Scale bytes of a tile by bulk copies where a box's lie side by side: 4 capped trees of 64 nodes 358 us, by plain loads 477 us (before the widening's last change).
   a.q8.bulk = cache->scale_token_stride == nb && (box * nb) % 16 == 0 && q8_scales_box(&one, box * nb);
   if (maps && few) {
     a.kt = 16;

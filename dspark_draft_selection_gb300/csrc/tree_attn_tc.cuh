@@ -21,9 +21,9 @@
 // warp 1 issues the MMAs; warp 3 copies the query rows; warps 4-7 and 8-11 are the softmax groups.
 // Q8: warp 0 copies the codes of both, and their scale bytes, into a ring of their own, and warps 12-15, a thread a key, write them as
 // bf16 numbers (exactly: a code has at most seven bits of fraction and a scale is a power of two) into the stages that the MMAs take. The
-// weights, sums and joins are the same. What bounds it is the issue of the widening beside the softmax, two instructions a number and 512
-// threads of 128 registers: 4 capped trees of 64 nodes x 8 heads, 40,000-65,600 keys 358 us, 530 TFLOP/s (with a bf16 cache 250 us); 32 requests of 16 nodes
-// x 4 heads, 300-8,200 keys 205 us (127 us).
+// weights, sums and joins are the same. What bounds it is the widening's arithmetic beside the softmax, two instructions a number, and 512
+// threads of 128 registers: 4 capped trees of 64 nodes x 8 heads, 40,000-65,600 keys 340 us, 560 TFLOP/s (with a bf16 cache 250 us; without
+// the widening's instructions the kernel takes as long as over a bf16 cache); 32 requests of 16 nodes x 4 heads, 300-8,200 keys 195 us (127 us).
 // Bound: HBM (2 D bytes of keys and of values per cached token and key head) up to about 128 query rows per
 // key head, above that the chain P V, Q K^T, softmax of a group: S and P share their tensor memory (S, O of
 // both groups take all 512 columns), so a group's next scores wait for its P V. Measured with the join:
@@ -277,7 +277,9 @@ __device__ __noinline__ void ta_add_odd(const TaArgs& a, int r, int32_t ctx, int
 
 // A row of codes of one key as bf16 numbers into the tile that the MMAs take. A thread a key; `w4`: the scale bytes of its
 // blocks. Rows go to different banks within each 8 lanes on both sides. E4M3: the seven bits under the sign go to bits 10..4 of a bf16 number,
-// which is then the number times 2^-120; INT8: 128 + (low seven bits) - 128 (1 + sign).
+// which is then the number times 2^-120, and the sign, which goes to bit 11 with them, on to bit 15 (2^11 + 240 * 2^7 = 2^15); INT8: 128 + (low seven
+// bits) - 128 (1 + sign). What counts is how few instructions of the logic pipe this takes, which the softmax needs too: with the shift as a
+// multiplication and one factor for scales up to 2^7 340 us (4 capped trees of 64 nodes), with shifts, masks and always two factors 358 us.
 template <int DP, bool E4M3>
 DS_DEV void ta_widen_row(const uint8_t* raw, uint8_t* tile, int row, uint32_t w4) {
   auto mul2 = [](uint32_t x, uint32_t y) {
@@ -299,24 +301,32 @@ DS_DEV void ta_widen_row(const uint8_t* raw, uint8_t* tile, int row, uint32_t w4
   for (int c = 0; c < DP / 16; ++c) {                  // (a loop: unrolled, its code takes the others' place in the instruction caches)
     const uint4 x = *reinterpret_cast<const uint4*>(raw + row * DP + ((c ^ (DP == 128 ? row & 7 : (row >> 1) & 3)) << 4));
     const uint32_t b = q8_byte((w4 >> (8 * (c >> 1))) & 0xFFu);
-    const uint32_t f = (E4M3 ? min(b + 120u, 254u) : b) * 0x00800080u, f2 = (127u + (b > 134u ? b - 134u : 0u)) * 0x00800080u;
+    const uint32_t f = (E4M3 ? min(b + 120u, 254u) : b) * 0x00800080u;
     uint32_t y[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t w = e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w;
-      const uint32_t lo = __byte_perm(w, 0u, 0x1404), hi = __byte_perm(w, 0u, 0x3424);   // two codes in the high bytes of the halves
+      const uint32_t lo = __byte_perm(w, 0u, 0x4140), hi = __byte_perm(w, 0u, 0x4342);   // two codes, one a half
       if (E4M3) {
-        y[2 * e] = mul2(mul2(pick(lo, 0x80008000u, (lo >> 4) & 0x07F007F0u), f), f2);
-        y[2 * e + 1] = mul2(mul2(pick(hi, 0x80008000u, (hi >> 4) & 0x07F007F0u), f), f2);
+        y[2 * e] = mul2(lo * 16u + (lo & 0x00800080u) * 240u, f);
+        y[2 * e + 1] = mul2(hi * 16u + (hi & 0x00800080u) * 240u, f);
       } else {
-        const uint32_t l8 = lo >> 8, h8 = hi >> 8;
-        y[2 * e] = mul2(sub2(pick(l8, 0x007F007Fu, 0x43004300u), pick(l8, 0x00800080u, 0x43004300u)), f);
-        y[2 * e + 1] = mul2(sub2(pick(h8, 0x007F007Fu, 0x43004300u), pick(h8, 0x00800080u, 0x43004300u)), f);
+        y[2 * e] = mul2(sub2(pick(lo, 0x007F007Fu, 0x43004300u), pick(lo, 0x00800080u, 0x43004300u)), f);
+        y[2 * e + 1] = mul2(sub2(pick(hi, 0x007F007Fu, 0x43004300u), pick(hi, 0x00800080u, 0x43004300u)), f);
       }
     }
     uint8_t* to = tile + (c >> 2) * TA_CHUNK + row * 128;
     *reinterpret_cast<uint4*>(to + ((((2 * c) & 7) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
     *reinterpret_cast<uint4*>(to + ((((2 * c + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+  }
+  if (E4M3 && (((w4 & 0x7F7F7F7Fu) + 0x79797979u) & w4 & 0x80808080u)) {     // a byte above 134: the rest of a power that one factor does not reach
+#pragma unroll 1
+    for (int c = 0; c < DP / 8; ++c) {
+      const uint32_t b = q8_byte((w4 >> (8 * (c >> 2))) & 0xFFu), f = (127u + (b > 134u ? b - 134u : 0u)) * 0x00800080u;
+      uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * TA_CHUNK + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+      const uint4 x = *at;
+      *at = make_uint4(mul2(x.x, f), mul2(x.y, f), mul2(x.z, f), mul2(x.w, f));
+    }
   }
 }
 

@@ -138,6 +138,23 @@ def test_far_scales(T):
             assert np.abs(got - want).max() <= 2.0 ** -6 * np.abs(want).max() + 2.0 ** -126
 
 
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("T", [3, 20, 70])
+def test_scales_on_both_sides_of_2_to_the_7(T, code, head_dim):
+    """Blocks of a value row, and rows of a tile, whose powers of two lie below and above what one bf16 factor reaches over E4M3 codes."""
+    c = Q8Case(T, T, 4, 2, head_dim, 16, [150], None, "bf16", code, mask="chain")
+    v = c.cache[3]
+    v.copy_(torch.randint(128, 142, v.shape, device="cuda").to(torch.uint8))
+    c.k, c.v = numbers(c.cache, code)
+    c.run()
+    at = torch.arange(150 + T, device="cuda")
+    k, x = (t[c.table[0].long()[at // 16], at % 16].cpu().numpy() for t in (c.k, c.v))
+    want, _, mag, _ = tree.attention(c.q[0].double().cpu().numpy(), k, x, np.concatenate([np.ones((T, 150), bool), np.tri(T, dtype=bool)], 1), c.scale)
+    # a weight, its sum's share and the result are off by half a step of bf16 each, the weight twice that where the sum is the unrounded one
+    assert (np.abs(c.out[0].double().cpu().numpy() - want) <= 2.0 ** -7 * mag + 2.0 ** -8 * np.abs(want)).all()
+
+
 @pytest.mark.parametrize("T", [1, 8, 40])
 def test_what_nobody_sees_changes_no_bit(T):
     """Stale codes and scales of any value behind the sequences, in unseen pages, and infinite queries of other rows."""
