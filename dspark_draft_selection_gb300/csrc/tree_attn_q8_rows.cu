@@ -40,6 +40,8 @@ constexpr int TQ_KEYS = 16;                  // keys of a slice
 constexpr float TQ_TOP = 15.0f;              // weights reach 2^15;
 constexpr float TQ_AT = 7.0f;                // a new reference gives the largest score a weight of 2^7
 constexpr float TQ_NONE = -3e38f;            // reference of a row that has seen nothing
+constexpr uint32_t TQ_FAR = 170;             // largest scale byte that O is relative to: 2^15 * 448 * 2^(245 - 170) times 2^28 keys is a float32
+                                             // number, and values whose byte is 53 or more are exact bf16 numbers relative to it
 
 template <int DP, int NQ>
 struct TqLayout {
@@ -484,6 +486,8 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
         ek = __reduce_max_sync(0xFFFFFFFFu, mk);
 #pragma unroll
         for (int x = 1; x < (DP == 128 ? 8 : 16); x <<= 1) mv = max(mv, __shfl_xor_sync(0xFFFFFFFFu, mv, x));   // the lanes of a block: all four t4, two or four g
+        // (No reference lies above TQ_FAR: rows that do not see the largest values keep theirs. Larger ones take the bf16 forms.)
+        mv = min(mv, TQ_FAR);
         if (ev == 0u || mv > ev + HI - 15u) {
           const int down = int(ev) - int(mv);          // 2^down, in two steps where it is small
           const float f = __uint_as_float(uint32_t(max(down, -126) + 127) << 23), f2 = __uint_as_float(uint32_t(max(down + 126, -126) + 127) << 23);

@@ -175,6 +175,24 @@ def test_what_nobody_sees_changes_no_bit(T):
     assert torch.equal(c.out, first) and torch.equal(c.lse, lse)
 
 
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("T,Hq", [(2, 4), (4, 8), (8, 8), (40, 4)])
+def test_the_largest_values_in_a_node_that_others_do_not_see(T, Hq, code):
+    """The last node of a chain has values near float32's largest, all others small ones: the rows before it keep their accuracy."""
+    c = Q8Case(T, T, Hq, 2, 128, 16, [70], None, "bf16", code, mask="chain")
+    v = c.cache[3]
+    v.copy_(torch.randint(88, 110, v.shape, device="cuda").to(torch.uint8))
+    last = 70 + T - 1
+    v[c.table[0, last // 16].long(), last % 16] = 245
+    c.k, c.v = numbers(c.cache, code)
+    c.run()
+    at = torch.arange(70 + T, device="cuda")
+    k, x = (t[c.table[0].long()[at // 16], at % 16].cpu().numpy() for t in (c.k, c.v))
+    want, _, mag, _ = tree.attention(c.q[0].double().cpu().numpy(), k, x, np.concatenate([np.ones((T, 70), bool), np.tri(T, dtype=bool)], 1), c.scale)
+    # a weight, its sum's share and the result are off by half a step of bf16 each, the weight twice that where the sum is the unrounded one
+    assert (np.abs(c.out[0].double().cpu().numpy() - want) <= 2.0 ** -7 * mag + 2.0 ** -8 * np.abs(want)).all()
+
+
 @pytest.mark.parametrize("T", [1, 3, 40])
 def test_a_query_that_is_not_finite_stays_in_its_row(T):
     c = Q8Case(T, T, 8, 2, 64, 16, [130], None, "bf16", "int8", mask="chain").run()
