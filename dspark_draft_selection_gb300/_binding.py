@@ -724,7 +724,8 @@ def dspark_tree_attention_q8(q, cache, page_table, ctx_len, *, mask=None, n_node
 
 
 def dspark_cache_commit_q8(cache, page_table, ctx_len, path, n_accepted, *, T=None, out=None, status=None, stream=None):
-    """dspark_cache_commit for a cache in 8 bits (q8_cache, every layer of it). Returns (new_len [R], status)."""
+    """dspark_cache_commit for a cache in 8 bits (q8_cache, every layer of it). Returns (new_len [R], status). out shares no memory with
+    ctx_len, path or n_accepted (without path it may be n_accepted itself)."""
     if stream is not None:
         return _on(stream, dspark_cache_commit_q8, locals())
     c, _, _, R = _qcache(cache, page_table)

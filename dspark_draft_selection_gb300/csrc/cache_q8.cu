@@ -516,7 +516,7 @@ extern "C" dspark_status dspark_cache_commit_q8(const dspark_qcache* cache, cons
                                                 int32_t* dev_status, dspark_stream_t stream) {
   DS_REQUIRE(q8_cache_ok(cache, true) && cache->n_layers <= (1 << 20) && R >= 0 && R <= 65535 && T >= 1 && T <= QC_MAXT);
   if (R == 0) return DSPARK_OK;
-  DS_REQUIRE(ctx_len && n_accepted && new_len && dev_status && new_len != ctx_len);
+  DS_REQUIRE(ctx_len && n_accepted && new_len && dev_status && ds_commit_len_ok(new_len, ctx_len, n_accepted, path, R, T));
   const dim3 grid(path ? 2 * unsigned(cache->n_layers) : 1u, unsigned(R));
   const bool v16 = cache->head_dim % 16 == 0 && q8_codes_aligned(cache, 16), v8 = q8_codes_aligned(cache, 8);
   const bool s4 = q8_blocks(cache->head_dim) % 4 == 0 && q8_scales_aligned(cache, 4);

@@ -37,6 +37,12 @@ static inline bool ds_aligned(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
+// Whether `na` bytes from a and `nb` bytes from b (null: none) share one.
+static inline bool ds_overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 // Poll limit of the first wait for a tile's tensor-core MMAs (lattice and dense walk); lowered only
 // by the test hook dspark_test_set_first_wait_polls.
 extern std::atomic<uint32_t> g_ds_first_wait_polls;
@@ -82,6 +88,15 @@ static inline bool ds_cache_ok(const dspark_kvcache* c, bool layers) {
          c->head_stride >= 0 && c->num_pages >= 1 && c->num_pages <= INT32_MAX && c->page_size >= 1 &&
          c->page_size <= 65536 && c->heads >= 1 && c->heads <= 1024 && c->head_dim >= 8 && c->head_dim <= 256 &&
          c->head_dim % 8 == 0 && c->table_pages >= 1 && c->ld_table >= c->table_pages && (!layers || (c->n_layers >= 1 && c->layer_stride >= 0));
+}
+
+// new_len of a commit may overlap nothing that the blocks of other buffers and layers read after one block has written it. Without a path
+// there is one block a request, which has read its count by then: new_len may be n_accepted itself.
+static inline bool ds_commit_len_ok(const int32_t* new_len, const int32_t* ctx_len, const int32_t* n_accepted, const int32_t* path, int64_t R,
+                                    int32_t T) {
+  const size_t n = size_t(R) * 4;
+  if (ds_overlap(new_len, n, ctx_len, n) || ds_overlap(new_len, n, path, n * size_t(T))) return false;
+  return (!path && new_len == n_accepted) || !ds_overlap(new_len, n, n_accepted, n);
 }
 
 // Every row of every head of the cache starts on a 16-byte boundary.

@@ -581,7 +581,8 @@ dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, dspark_dtype 
                                        int32_t* dev_status, dspark_stream_t stream);
 
 /*
- * dspark_cache_commit for a cache in 8 bits: codes and scales move, the numbers stay what they were.
+ * dspark_cache_commit for a cache in 8 bits: codes and scales move, the numbers stay what they were. new_len overlaps neither ctx_len
+ * nor path nor n_accepted (without path it may be n_accepted itself): DSPARK_EINVAL.
  */
 dspark_status dspark_cache_commit_q8(const dspark_qcache* cache, const int32_t* ctx_len,
                                      const int32_t* path, const int32_t* n_accepted, int64_t R, int32_t T,
