@@ -608,7 +608,8 @@ def dspark_cache_commit(k_cache, v_cache, page_table, ctx_len, path, n_accepted,
                         stream=None):
     """Moves the accepted nodes' rows (path [R, T], n_accepted [R] int32) to the front of their requests'
     drafted slots, in every layer of k_cache / v_cache ([layers, pages, page, heads, head_dim] or one
-    layer). path None: chains of T nodes, only the length changes. Returns (new_len [R], status)."""
+    layer). path None: chains of T nodes, only the length changes. Returns (new_len [R], status). out shares no memory with
+    ctx_len, path or n_accepted (without path it may be n_accepted itself)."""
     if stream is not None:
         return _on(stream, dspark_cache_commit, locals())
     c, _, _, R = _kvcache(k_cache, v_cache, page_table)

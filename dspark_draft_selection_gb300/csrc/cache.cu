@@ -338,7 +338,7 @@ extern "C" dspark_status dspark_cache_commit(const dspark_kvcache* cache, const 
                                              int32_t* dev_status, dspark_stream_t stream) {
   DS_REQUIRE(ds_cache_ok(cache, true) && cache->n_layers <= (1 << 20) && R >= 0 && R <= 65535 && T >= 1 && T <= CM_MAXT);
   if (R == 0) return DSPARK_OK;
-  DS_REQUIRE(ctx_len && n_accepted && new_len && dev_status && new_len != ctx_len);
+  DS_REQUIRE(ctx_len && n_accepted && new_len && dev_status && ds_commit_len_ok(new_len, ctx_len, n_accepted, path, R, T));
   const dim3 grid(path ? 2 * unsigned(cache->n_layers) : 1u, unsigned(R));
   const bool vec = ds_cache_vec(cache) && (cache->head_dim * ds_dtype_size(cache->dtype)) % 16 == 0;
   if (cache->dtype == DSPARK_BF16) {

@@ -506,7 +506,8 @@ dspark_status dspark_tree_accept(const int32_t* tokens, const int32_t* parent, c
 /*
  * Keeps the accepted nodes: for k = 0..n_accepted[r], in every layer, slot ctx_len[r] + path[r, k]
  * of the keys and values moves to slot ctx_len[r] + k, and new_len[r] = ctx_len[r] + n_accepted[r]
- * + 1 (new_len [R] int32 device, not ctx_len itself). path [R, T] int32 ascending, as
+ * + 1 (new_len [R] int32 device; it overlaps neither ctx_len nor path nor n_accepted, but without path it may be
+ * n_accepted itself: DSPARK_EINVAL). path [R, T] int32 ascending, as
  * dspark_tree_accept writes it; NULL: a chain, nothing moves. n_accepted < 0: nothing moves and the
  * length stays. n_accepted >= T, or a path entry that is not above the one before and below T, sets
  * DSPARK_EINVAL on *dev_status and leaves that request as it was. T 1..512, R <= 65535.
@@ -581,8 +582,7 @@ dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, dspark_dtype 
                                        int32_t* dev_status, dspark_stream_t stream);
 
 /*
- * dspark_cache_commit for a cache in 8 bits: codes and scales move, the numbers stay what they were. new_len overlaps neither ctx_len
- * nor path nor n_accepted (without path it may be n_accepted itself): DSPARK_EINVAL.
+ * dspark_cache_commit for a cache in 8 bits: codes and scales move, the numbers stay what they were.
  */
 dspark_status dspark_cache_commit_q8(const dspark_qcache* cache, const int32_t* ctx_len,
                                      const int32_t* path, const int32_t* n_accepted, int64_t R, int32_t T,

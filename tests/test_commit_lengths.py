@@ -8,7 +8,7 @@ import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 EINVAL = 1
-CALLS = ["dspark_cache_commit_q8"]
+CALLS = ["dspark_cache_commit_q8", "dspark_cache_commit"]
 
 
 @pytest.fixture(scope="module")
