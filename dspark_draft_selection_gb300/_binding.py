@@ -639,19 +639,31 @@ def q8_cache(pages, page, heads, head_dim, *, layers=None, dtype=torch.float8_e4
     return (*codes, *scales)
 
 
-def _here(t):
-    """The kernels run on the current device: a tensor of another is refused."""
-    if t.is_cuda:
-        here = _device()
-        if here is not None and t.get_device() != here:
-            raise ValueError(f"a tensor of {t.device}, but the current device is cuda:{here}: call within torch.cuda.device({t.get_device()})")
+_devices = None        # how many devices the process sees, once one of its tensors has been seen
+
+
+def _here(first, *others):
+    """The kernels run on the current device: tensors of another (None: no tensor) are refused. Where there is one device, which
+    the others then cannot differ in, they are not looked at (1.2 us a call)."""
+    global _devices
+    at = first.get_device()
+    if at < 0:
+        return                                             # a tensor of the host: _p refuses it
+    here = _device()
+    if here is None:
+        here = torch.cuda.current_device()
+    if _devices is None:
+        _devices = torch.cuda.device_count()
+    for t in (first,) if at == here and _devices == 1 else (first, *others):
+        at = here if t is None else t.get_device()
+        if at != here and at >= 0:
+            raise ValueError(f"a tensor of {t.device}, but the current device is cuda:{here}: call within torch.cuda.device({at})")
 
 
 def _qcache(cache, page_table):
     """(bytes of a dspark_qcache, heads, head_dim, requests) of cache = (k, v, k_scale, v_scale) as q8_cache makes it (any strides, the
     last 1) and page_table [R, n]."""
     k, v, ks, vs = cache
-    _here(k)
     sh, st, ssh, sst = k.shape, k.stride(), ks.shape, ks.stride()
     if v.shape != sh or v.stride() != st or v.dtype is not k.dtype:
         raise ValueError("keys and values are of one shape, layout and type")
@@ -677,6 +689,7 @@ def dspark_rope_append_q8(q, k, v, pos, cos_sin, cache, page_table, ctx_len, *, 
     and v, quantised, to the nodes' slots. Returns (q_out, status); out may be q itself."""
     if stream is not None:
         return _on(stream, dspark_rope_append_q8, locals())
+    _here(q, k, v, pos, cos_sin, *cache, page_table, ctx_len, axis, n_nodes, out, status)
     qs = q.shape
     R, T, Hq, D = qs
     c, H, Dc, Rt = _qcache(cache, page_table)
@@ -702,6 +715,7 @@ def dspark_tree_attention_q8(q, cache, page_table, ctx_len, *, mask=None, n_node
     are in the cache. ws: workspace(OP_TREE_ATTENTION_Q8, R, T, Hq * D, H). Returns (out, lse, status)."""
     if stream is not None:
         return _on(stream, dspark_tree_attention_q8, locals())
+    _here(q, *cache, page_table, ctx_len, mask, n_nodes, out, lse if lse is not False else None, ws, status)
     qs = q.shape
     R, T, Hq, D = qs
     c, H, Dc, Rt = _qcache(cache, page_table)
@@ -716,7 +730,9 @@ def dspark_tree_attention_q8(q, cache, page_table, ctx_len, *, mask=None, n_node
     elif lse.shape != (R, T, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous():
         raise ValueError("expected a contiguous float32 lse [R, T, Hq]")
     status = new_status(q.device) if status is None else status
-    wp, wn = _ws(workspace(OP_TREE_ATTENTION_Q8, R, T, Hq * D, H, q.device) if ws is None else ws)
+    ws = workspace(OP_TREE_ATTENTION_Q8, R, T, Hq * D, H, q.device) if ws is None else ws
+    _p(ws)                                                 # a device tensor
+    wp, wn = _ws(ws)
     _check(lib().dspark_tree_attention_q8(_p(q), _node_rows(q, qs, dt), _dt(q), R, T, Hq, c, _i32(ctx_len, R), _i32(n_nodes, R),
                                           _i32(mask, R, T, (T + 31) // 32), D ** -0.5 if scale is None else scale, softcap,
                                           _p(out), _node_rows(out, qs, dt), _p(lse), wp, wn, _p(status), _stream(stream)),
@@ -729,6 +745,7 @@ def dspark_cache_commit_q8(cache, page_table, ctx_len, path, n_accepted, *, T=No
     ctx_len, path or n_accepted (without path it may be n_accepted itself)."""
     if stream is not None:
         return _on(stream, dspark_cache_commit_q8, locals())
+    _here(*cache, page_table, ctx_len, path, n_accepted, out, status)
     c, _, _, R = _qcache(cache, page_table)
     if path is not None:
         T = path.shape[1]
@@ -745,6 +762,7 @@ def dspark_cache_read_q8(cache, page_table, n, *, start=None, S=None, dtype=torc
     (k, v) of one layout, whose rows past n[r] are left as they were."""
     if stream is not None:
         return _on(stream, dspark_cache_read_q8, locals())
+    _here(*cache, page_table, n, start, *(out or ()), status)
     if out is None and S is None:
         raise ValueError("S, the rows of a request, or out has to be given")
     c, H, D, R = _qcache(cache, page_table)
@@ -786,7 +804,7 @@ def dspark_tree_verify(p, tokens, parent, u_accept, u_draw, *, q=None, n_nodes=N
     status) as dspark_tree_accept does."""
     if stream is not None:
         return _on(stream, dspark_tree_verify, locals())
-    _here(p)
+    _here(p, tokens, parent, u_accept, u_draw, q, n_nodes, *(out or ()), status)
     R, T = tokens.shape
     V = p.shape[-1]
     dev = tokens.device
