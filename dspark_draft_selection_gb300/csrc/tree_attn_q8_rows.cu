@@ -501,6 +501,39 @@ tree_attn_q8_rows_kernel(const TaArgs a, const __grid_constant__ CUtensorMap tmK
         }
         // references at which no byte in reach of one is read as another
         near = ek >= 16u && ek <= 230u && ((narrow && g * (DP / 8) >= D) || (ev >= 16u && ev <= 230u));
+        // A block of zeros, which is written under the least power, has code 0 under any: out of the references' reach it counts as one that is not there
+        // instead of sending the slice to the bf16 forms, whose weights have three bits less. (With one in every slice 64 single tokens take 151 us, in
+        // those forms 185 us, 32 requests of 8 nodes 206 and 298 us; with none 126 and 187 us.)
+        const bool far_k = ek > 15u, far_v = ev > 15u;
+        constexpr uint32_t DIGITS = E4M3 ? 0x7F7F7F7Fu : 0xFFFFFFFFu;      // (minus zero)
+        if (__any_sync(0xFFFFFFFFu, far_k && min(kb[0], kb[1]) == 1u)) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint8_t* row = K + (8 * x + g) * DP;
+            uint4 y = *reinterpret_cast<const uint4*>(row + (DP == 128 ? (2 * t4) ^ g : t4 ^ (g >> 1)) * 16);
+            uint32_t any = y.x | y.y | y.z | y.w;
+            if (DP == 128) {
+              y = *reinterpret_cast<const uint4*>(row + ((2 * t4 + 1) ^ g) * 16);
+              any |= y.x | y.y | y.z | y.w;
+            }
+            if (far_k && kb[x] == 1u && (any & DIGITS) == 0u) gone |= 1u << x;
+          }
+        }
+        if (__any_sync(0xFFFFFFFFu, far_v && min(min(vb[0], vb[1]), min(vb[2], vb[3])) == 1u)) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = 2 * t4 + (x & 1) + 8 * (x >> 1);
+            uint32_t any;
+            if constexpr (DP == 128) {
+              const uint4 y = *reinterpret_cast<const uint4*>(V + key * DP + ((g ^ (key & 7)) << 4));
+              any = y.x | y.y | y.z | y.w;
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(V + key * DP + (((g >> 1) ^ ((key >> 1) & 3)) << 4) + (g & 1) * 8);
+              any = y.x | y.y;
+            }
+            if (far_v && vb[x] == 1u && (any & DIGITS) == 0u) gone |= 4u << x;
+          }
+        }
         tame = __all_sync(0xFFFFFFFFu, relative());    // with the bytes cut to their range
       }
       auto slice = [&](auto far) {
