@@ -33,7 +33,7 @@ struct TvShared {
   FF warp[WARPS], part[2][TV_MAXC];       // stretches of this block; shares of all blocks, two rounds of them
   uint32_t filter[64];                       // a bit for every refused id modulo 2048 (q absent)
   FF a;
-  int32_t cur, done, known, refused, depth;  // row asked for; whether the walk ended, and its sum is known; first refused child (q absent), depth
+  int32_t cur, done, refused, depth;         // row asked for; whether the walk ended; first refused child (q absent), depth
 };
 
 DS_DEV FF tv_pair(double x) {
@@ -200,7 +200,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) tree_verify_kernel(co
         s.depth = depth;
         s.refused = s.first[cur];
         s.a = tv_pair(da);
-        s.known = Q && !open && !plain && da != 0.0;
       }
       __syncthreads();
       const bool done = s.done != 0;
@@ -212,7 +211,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) tree_verify_kernel(co
           if (!plain && s.par[k] == s.cur && s.tok[k] >= 0) atomicOr(&s.filter[(s.tok[k] >> 5) & 63], 1u << (s.tok[k] & 31));
         __syncthreads();
       }
-      const bool known = done && s.known != 0;         // the row's sum is the last one
       const int64_t row = r * T + s.cur;
       const float* pr = a.p + row * a.ldp;
       const float* qr = Q ? a.q + row * a.ldq : nullptr;
@@ -235,54 +233,52 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) tree_verify_kernel(co
         }
         return false;
       };
-      if (!known) {
-        const bool some = span(lo, hi);
-        FF acc[4] = {};
-        // four vectors of each row on their way together
-        for (int64_t i = lo + lane * 4; i < hi; i += 32 * 16) {
-          float4 x[4], y[4];
+      const bool some = span(lo, hi);
+      FF acc[4] = {};
+      // four vectors of each row on their way together
+      for (int64_t i = lo + lane * 4; i < hi; i += 32 * 16) {
+        float4 x[4], y[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            x[c] = tv_load<VEC>(pr, i + 128 * c, hi);
-            if (minus) y[c] = tv_load<VEC>(qr, i + 128 * c, hi);
+        for (int c = 0; c < 4; ++c) {
+          x[c] = tv_load<VEC>(pr, i + 128 * c, hi);
+          if (minus) y[c] = tv_load<VEC>(qr, i + 128 * c, hi);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (some) {
+            const int64_t id = i + 128 * c;
+            x[c] = make_float4(gone(id) ? 0.0f : x[c].x, gone(id + 1) ? 0.0f : x[c].y, gone(id + 2) ? 0.0f : x[c].z, gone(id + 3) ? 0.0f : x[c].w);
           }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (some) {
-              const int64_t id = i + 128 * c;
-              x[c] = make_float4(gone(id) ? 0.0f : x[c].x, gone(id + 1) ? 0.0f : x[c].y, gone(id + 2) ? 0.0f : x[c].z, gone(id + 3) ? 0.0f : x[c].w);
-            }
-            if (minus) {
-              tv_add(acc[0], tv_term<true>(x[c].x, y[c].x, fa));
-              tv_add(acc[1], tv_term<true>(x[c].y, y[c].y, fa));
-              tv_add(acc[2], tv_term<true>(x[c].z, y[c].z, fa));
-              tv_add(acc[3], tv_term<true>(x[c].w, y[c].w, fa));
-            } else {
-              tv_add(acc[0], tv_term<false>(x[c].x, 0.0f, fa));
-              tv_add(acc[1], tv_term<false>(x[c].y, 0.0f, fa));
-              tv_add(acc[2], tv_term<false>(x[c].z, 0.0f, fa));
-              tv_add(acc[3], tv_term<false>(x[c].w, 0.0f, fa));
-            }
+          if (minus) {
+            tv_add(acc[0], tv_term<true>(x[c].x, y[c].x, fa));
+            tv_add(acc[1], tv_term<true>(x[c].y, y[c].y, fa));
+            tv_add(acc[2], tv_term<true>(x[c].z, y[c].z, fa));
+            tv_add(acc[3], tv_term<true>(x[c].w, y[c].w, fa));
+          } else {
+            tv_add(acc[0], tv_term<false>(x[c].x, 0.0f, fa));
+            tv_add(acc[1], tv_term<false>(x[c].y, 0.0f, fa));
+            tv_add(acc[2], tv_term<false>(x[c].z, 0.0f, fa));
+            tv_add(acc[3], tv_term<false>(x[c].w, 0.0f, fa));
           }
         }
-        rs::ff_acc(acc[0], acc[1]);
-        rs::ff_acc(acc[2], acc[3]);
-        rs::ff_acc(acc[0], acc[2]);
-        const FF w = rs::warp_ff_reduce(acc[0]);
-        if (lane == 0) s.warp[warp] = w;
-        __syncthreads();
-        if (tid < ranks) {
-          FF sum = s.warp[0];
-          for (int k = 1; k < WARPS; ++k) rs::ff_acc(sum, s.warp[k]);
-          if (ranks > 1) tv_put_remote(&s.part[round & 1][rank], tid, sum);
-          else s.part[round & 1][0] = sum;
-        }
-        if (ranks > 1) tv_cluster_sync();
-        else __syncthreads();
-        total = FF{0.0f, 0.0f};
-        for (int k = 0; k < ranks; ++k) rs::ff_acc(total, s.part[round & 1][k]);
-        ++round;
       }
+      rs::ff_acc(acc[0], acc[1]);
+      rs::ff_acc(acc[2], acc[3]);
+      rs::ff_acc(acc[0], acc[2]);
+      const FF w = rs::warp_ff_reduce(acc[0]);
+      if (lane == 0) s.warp[warp] = w;
+      __syncthreads();
+      if (tid < ranks) {
+        FF sum = s.warp[0];
+        for (int k = 1; k < WARPS; ++k) rs::ff_acc(sum, s.warp[k]);
+        if (ranks > 1) tv_put_remote(&s.part[round & 1][rank], tid, sum);
+        else s.part[round & 1][0] = sum;
+      }
+      if (ranks > 1) tv_cluster_sync();
+      else __syncthreads();
+      total = FF{0.0f, 0.0f};
+      for (int k = 0; k < ranks; ++k) rs::ff_acc(total, s.part[round & 1][k]);
+      ++round;
       if (!done) continue;
       const float mass = __fadd_rn(total.hi, total.lo);
       if (!(mass > 0.0f) && mass == mass && !plain) {  // nothing left: p itself
