@@ -118,7 +118,8 @@ DS_DEV void qa_turn(const T* head, int d, int rot, bool interleaved, const float
 // the heads' items of VEC columns: queries, keys, values. The 32 / VEC neighbouring threads that hold a block of 32 columns find its largest
 // magnitude by shuffles, so a column is loaded once and its code needs no second pass. Every byte moves once. 15,000 rows of 32 + 2 x 8 heads of 128
 // in bf16: 68 us, 4.6 TB/s; the queries' part of it runs at the rate of HBM, the keys' and values' part (39 us of them) is bound by the instructions of
-// rotation, magnitude and conversion. Few rows are bound by the latency of the lookups: 8 rows 3 us of the GPU.
+// rotation, magnitude and conversion. Few rows are bound by the latency of the lookups: 8 rows 3 us of the GPU. Two rows a block are compiled for 14 blocks
+// an SM, 32 registers with 12 bytes of spills (68 us; for 12 blocks, 40 registers and no spills, 73 us, for 10 blocks 76 us; float32 101, 99 and 99 us).
 template <typename T, int VEC, int NR>
 __global__ void __launch_bounds__(QA_THREADS, NR > 1 ? 14 : 1) rope_append_q8_kernel(const QaArgs a) {
   constexpr int GROUP = Q8_BLOCK / VEC;                // threads of a block of columns

@@ -65,7 +65,7 @@ extern "C" dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, ds
   };
   DS_REQUIRE(counts(64));
   // Few rows a key head: the kernel that widens codes in operand registers; more: the one that stages them for tcgen05, which takes the same
-  // time whatever the rows up to 128. 300-8,200 keys: 64 requests with 4 rows 127 and 383 us; 32 requests with 16 rows 103 and 195 us, with 32 rows 187 and
+  // time whatever the rows up to 128. 300-8,200 keys: 64 requests with 4 rows 126 and 383 us; 32 requests with 16 rows 105 and 195 us, with 32 rows 187 and
   // 185 us, but 197 and more than 270 us where scales lie by place and not by head.
   const bool few = a.rows <= 32;
   int box = few ? 16 : 128;

@@ -13,9 +13,10 @@
 //
 // Numbers. A code times a power of two from 2^-14 to 2^7 is an f16 number exactly. The powers of a slice's keys are taken relative to a
 // reference (the largest of the slice, for keys; a running one of each block of columns, for values, which O is relative to), and a slice whose
-// powers lie further apart takes bf16 forms with the full range instead. Queries go to f16 under a power of two of each row: what is below
-// 2^-38 of the row's largest is lost there, which is less than a float32 sum loses. Weights reach up to 2^15 and are rounded to f16's eleven
-// bits (2^-12 of a weight; those below 2^-32 of the row's largest to less).
+// powers lie further apart, blocks of zeros aside, takes bf16 forms with the full range instead. Queries go to f16 under a power of two of each row, the
+// largest to 2^13 .. 2^14: each column is off by at most 2^-25, 2^-38 of the largest. Weights are rounded to f16 relative to a reference at which the
+// row's largest is 2^7 to 2^15: by at most 2^-11 of a weight down to f16's least normal number (2^-21 to 2^-29 of the largest), below it by at most 2^-25,
+// which is 2^-32 of the largest or less (in the bf16 forms by 2^-8 of a weight). The sum that the result is divided by is of the unrounded weights.
 //
 // Every warp copies its own slices with TMA, NS of them in flight, and waits for nothing but its own barriers. The work is the line of
 // tiles of tree_attn.cuh with 16 keys a tile: a block's share is cut once more into its warps' shares; what two warps leave of an item is joined
@@ -23,10 +24,10 @@
 //
 // Bound by HBM (2 (D + D / 32) bytes a key and key head) for 4 rows a key head, by the latency of a warp's chain of scores, weights and
 // products for more (with 17 to 32 rows 255 registers a thread leave 8 warps an SM). Measured with the join, 300-8,200 keys, heads of 128, 8 of them:
-//   64 requests of one token x 4 heads    127 us   4.6 TB/s, 0.68 of the measured copy rate (with a bf16 cache 188 us)
-//   32 requests of 4 nodes x 4 heads      103 us
-//   32 requests of 8 nodes x 4 heads      189 us   (with a bf16 cache 114 us, whose kernel reads tiles as they lie)
-//   one token x 4 heads, 5,001 keys        19 us   with the host's call: two slices a warp, then the joins
+//   64 requests of one token x 4 heads    126 us   4.6 TB/s, 0.68 of the measured copy rate (with a bf16 cache 188 us)
+//   32 requests of 4 nodes x 4 heads      105 us
+//   32 requests of 8 nodes x 4 heads      187 us   (with a bf16 cache 114 us, whose kernel reads tiles as they lie)
+//   one token x 4 heads, 5,001 keys      17.6 us   with the host's call: two slices a warp, then the joins
 #include <cuda_fp16.h>
 
 #include <type_traits>

@@ -90,8 +90,8 @@ DS_DEV int tv_ranks() {
 // a row, each warp of the cluster taking one stretch of it. The stretches' sums then also say where the draw's target lies: the warp whose
 // stretch holds it reads it once more. Sums are float pairs, 2Sum and FMA, 48 bits: a token is drawn where a sum passes a border, and with
 // 10^5 ids a float32 sum would put one draw in a hundred on the other side. Bound by the sums that follow one another, one for a refusal that the
-// bound on b does not settle and one for the draw, each a pass over a row and a barrier of the cluster. Vocabularies of 151,936 ids: one tree without q 17 us
-// (with the call), 64 trees of 24 nodes with q 52 us, 1.5 TB/s of the rows that a draw cannot do without.
+// bound on b does not settle and one for the draw, each a pass over a row and a barrier of the cluster. Vocabularies of 151,936 ids: one tree without q 16 us
+// (with the call), 64 trees of 24 nodes with q 55 us (49-59 in eight runs), 1.4 TB/s of the rows that a draw cannot do without.
 template <bool Q, int VEC, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) tree_verify_kernel(const TvArgs a) {
   constexpr int WARPS = THREADS / 32;
@@ -433,7 +433,7 @@ extern "C" dspark_status dspark_tree_verify(const float* p, int64_t ldp, const f
   DS_REQUIRE(p && tokens && u_accept && u_draw && out_tokens && n_accepted && path && dev_status);
   DS_REQUIRE(ds_aligned(p, 4) && ds_aligned(q, 4) && ds_aligned(u_accept, 8) && ds_aligned(u_draw, 8));
   // Blocks for a request: as many as one wave of 1,024 threads an SM holds. With more requests than eight blocks of 512 threads each let into a
-  // wave, blocks have 256 threads: 64 trees of 24 nodes 52 us, with 512 threads 60 us; one tree 17 us with 512 threads, 21 us with 256. With four
+  // wave, blocks have 256 threads: 64 trees of 24 nodes 55 us, with 512 threads 59 us (means of eight runs); one tree 16 us with 512 threads, 21 us with 256. With four
   // blocks at most: one tree 23 us, 16 trees 47 us (36 us with eight), 64 trees 77 us; with one: 75, 140 and 219 us.
   const int64_t sms = ds_num_sms();
   const int threads = R * TV_MAXC > 2 * sms ? 256 : 512;

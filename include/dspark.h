@@ -570,9 +570,13 @@ dspark_status dspark_rope_append_q8(const void* q, int64_t ldq, const void* k, i
 /*
  * dspark_tree_attention over a cache in 8 bits: q and out are of `dtype`, the other arguments, the definition and the limits as
  * there, k and v being the numbers that the codes stand for. T = 1 without a mask is the attention of one new token. With bf16
- * queries the products run on the tensor cores and the weights p are rounded to bf16 for the product with v (head_dim a multiple of 16 up to
- * 128, page_size % 8 == 0, 16-byte aligned rows of codes, strides above 0; others in float32). ws: dspark_workspace_size(DSPARK_OP_TREE_ATTENTION_Q8, R, T,
- * Hq * head_dim, heads) bytes.
+ * queries the products run on the tensor cores (head_dim a multiple of 16 up to
+ * 128, page_size % 8 == 0, 16-byte aligned rows of codes, strides above 0; others in float32) and the weights p are rounded for the product with v:
+ * - more than 32 query rows a key head (T * Hq / heads): to bf16;
+ * - up to 32: to f16 (2^-11 of a weight, or 2^-32 of the row's largest weight where that is more), and a query's column is taken to within 2^-38 of its row's largest.
+ *   Where the powers of two of 16 neighbouring slots' keys, or of a block of columns' values and the largest before, lie more than 2^14 apart (blocks of zeros
+ *   aside), weights are rounded to bf16 and queries not at all.
+ * ws: dspark_workspace_size(DSPARK_OP_TREE_ATTENTION_Q8, R, T, Hq * head_dim, heads) bytes.
  */
 dspark_status dspark_tree_attention_q8(const void* q, int64_t ldq, dspark_dtype dtype, int64_t R,
                                        int32_t T, int32_t Hq, const dspark_qcache* cache,

@@ -107,3 +107,25 @@ def test_the_least_power_of_blocks_that_are_not_zeros(code, byte, T):
     # columns below 2^-126 may be read as 0
     tol = (eps[..., None] + 2.0 ** -8 * (1 + 2.0 ** -7)) * mag + 2.0 ** -8 * (1 + 2.0 ** -7) * np.abs(want) + 2.0 ** -126
     assert int(c.status) == 0 and (np.abs(f64(c.out[0]) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("T,Hq", [(1, 8), (4, 8), (8, 8), (40, 4)])
+@pytest.mark.parametrize("large", [1.0, 2.0 ** 12, 2.0 ** 26])
+def test_queries_of_a_wide_range(code, T, Hq, large):
+    """A block of query columns far above the others, where keys are zeros. With few rows a key head a query column is taken to within 2^-38 of its row's
+    largest, so a score is off by that times the sum of scale |k|, and a weight by the exponential of twice that (its own and the sum's)."""
+    c = Q8Case(T, T, Hq, 2, 128, 16, [21, 60], None, "bf16", code, mask="chain", scale=0.05)
+    q = c.q.clone()
+    q[..., 32:64] *= large
+    c.q = q
+    zero(c, 0, [1], 1).run()
+    for r in range(c.R):
+        end = c.ctx[r] + T
+        k, v = (f64(slots_of(x, c.table, r, end)) for x in (c.k, c.v))
+        x = f64(q[r])
+        want, _, mag, big = tree.attention(x, k, v, np.concatenate([np.ones((T, c.ctx[r]), bool), np.tri(T, dtype=bool)], 1), c.scale)
+        off = 2.0 ** -38 * c.scale * np.abs(x).max(-1) * np.abs(k).sum(-1).max() if T * Hq // 2 <= 32 else 0.0
+        eps = 2 * 136 * 2.0 ** -24 * big + 2.0 ** -20 + end * 2.0 ** -24 + np.expm1(2 * off)
+        tol = (eps[..., None] + 2.0 ** -8 * (1 + 2.0 ** -7)) * mag + 2.0 ** -8 * (1 + 2.0 ** -7) * np.abs(want) + 1e-30
+        assert int(c.status) == 0 and (np.abs(f64(c.out[r]) - want) <= tol).all()
