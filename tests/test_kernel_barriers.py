@@ -1,5 +1,5 @@
 """CPU check of the kernels' sources: a cluster's barrier in its `.aligned` form needs every thread of a warp to reach it together, which
-the compiler does not promise behind a branch on the thread's number or on data; the plain form may be reached by each thread for itself."""
+the compiler does not promise behind a branch on the thread's number or on data; the warp meets right before it, or the plain form is used."""
 import glob
 import os
 import re
@@ -7,10 +7,13 @@ import re
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "dspark_draft_selection_gb300", "csrc")
 
 
-def test_cluster_barriers_ask_for_no_converged_warp():
+def test_warps_meet_before_aligned_cluster_barriers():
     used = []
     for path in sorted(glob.glob(os.path.join(CSRC, "*"))):
-        for line in open(path).read().splitlines():
-            used += [(os.path.basename(path), x) for x in re.findall(r"barrier\.cluster\.\w+[.\w]*", line.split("//")[0])]
+        lines = [x.split("//")[0].strip() for x in open(path).read().splitlines()]
+        lines = [x for x in lines if x]
+        for before, line in zip([""] + lines, lines):
+            if re.search(r"barrier\.cluster\.", line):
+                used.append((os.path.basename(path), "aligned" not in line or before == "__syncwarp();"))
     assert used                                              # the pattern finds the barriers that there are
-    assert [u for u in used if "aligned" in u[1]] == []
+    assert all(ok for _, ok in used), used
